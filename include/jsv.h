@@ -63,10 +63,13 @@ typedef enum {
     JSV_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed       */
     JSV_ERR_TIMEOUT = 4,       /* a bounded device wait gave up              */
     JSV_ERR_DEVICE_INPUT = 5,  /* written to *dev_status: bad device data    */
-    JSV_ERR_BOUNDS = 6         /* written to *dev_status, only by a library
+    JSV_ERR_BOUNDS = 6,        /* written to *dev_status, only by a library
                                   built with JSV_CHECK_BOUNDS: a computed
                                   index fell outside its buffer (a library
                                   fault; the access was skipped)            */
+    JSV_ERR_NO_PAGES = 7       /* written to *dev_status: a page pool had too
+                                  few free pages for a request, which was
+                                  left as it was                            */
 } jsv_status;
 
 /*
@@ -303,6 +306,199 @@ JSV_API jsv_status jsv_lmhead_argmax_noalloc(const uint16_t *hidden, const uint1
                                              int32_t T, int32_t d, int32_t V,
                                              int32_t *argmax, float *max_logit,
                                              int32_t *dev_status, void *stream);
+
+/*
+ * 8-bit key/value cache.  The full 16-slot pages of a request's committed
+ * prefix are held as 8-bit codes with one fp32 scale for each (page, KV head)
+ * of K and of V; the last, partial page and the tree's slots stay in the bf16
+ * cache.  For request b with P_b prefix tokens:
+ *     slots [0, 16 * floor(P_b / 16))          8-bit pages, jsv_kv8.page_table
+ *     slots [16 * floor(P_b / 16), P_b + N_b)  bf16 pages, jsv_batch.page_table
+ * Both tables are indexed by logical page (slot / 16); jsv_batch.page_table
+ * entries below floor(P_b / 16) are not read, so their bf16 pages may be
+ * freed or shared out again.  A value is code * scale.
+ * Layout: codes [num_pages][Hkv][16][D] (the 16 x D block of one page and
+ * head is contiguous), scales [num_pages][Hkv].
+ * The pages that the README's engine keeps are bf16; this is a deployment
+ * form of the same cache with half its bytes.  Device pointers of these and
+ * the page pool's calls belong to the current device, whose stream is given.
+ */
+typedef enum {
+    JSV_KV8_E4M3 = 0,            /* 4-bit exponent, 3-bit mantissa, largest 448 */
+    JSV_KV8_INT8 = 1             /* two's complement, -128..127                 */
+} jsv_kv8_format;
+
+typedef struct {
+    int32_t format;              /* jsv_kv8_format                                */
+    int32_t num_pages;           /* physical pages in k and in v                  */
+    int32_t max_pages_per_req;   /* row stride of page_table                      */
+    uint8_t *k, *v;              /* device [num_pages][Hkv][16][D] codes, 16-B aligned */
+    float *k_scale, *v_scale;    /* device [num_pages][Hkv]                       */
+    const int32_t *page_table;   /* device [B][max_pages_per_req]                 */
+} jsv_kv8;
+
+/* Bytes of scratch jsv_tree_attention_kv8 needs for this geometry (split-KV
+ * partial results).  Depends on the host-side fields of both structures and
+ * on the current device's SM count; 0 when no request is split. */
+JSV_API size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, const jsv_kv8 *cache8);
+
+/*
+ * Tree-causal attention as jsv_tree_attention defines it, over a prefix whose
+ * full pages are read from the 8-bit cache (the last, partial page and the
+ * tree's own slots from the bf16 caches).  One node per request (node 0
+ * alone) is ordinary single-token decoding.  Scores, softmax statistics and
+ * the output are accumulated in fp32; the output is rounded to bf16.
+ *   q, scale, out, stream   as for jsv_tree_attention
+ *   k_cache, v_cache        the bf16 caches (batch->num_pages pages)
+ *   workspace, workspace_bytes  device scratch of at least
+ *            jsv_tree_attention_kv8_workspace_size() bytes, 256-B aligned
+ *            (NULL is accepted when that size is 0); any contents, written
+ *            and read within the call: calls that may overlap, graphs
+ *            replayed side by side included, take workspaces of their own
+ * Values that a node does not see do not reach its output, whatever they are
+ * (infinities and NaN in later slots of a page and in other branches of the
+ * tree included).  A node that sees a non-finite K or V value, or a
+ * non-finite scale, gets non-finite outputs (a visible non-finite value in
+ * the bf16 V cache makes all of the head's output NaN).
+ * Supported: D in {64, 128}; prefix pages need a row in each table.  The
+ * codes of a request's pages are trusted; page indices are checked.
+ */
+JSV_API jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
+                                          const uint16_t *k_cache, const uint16_t *v_cache, float scale,
+                                          uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Full pages of the bf16 cache written to the 8-bit cache.  For request b the
+ * logical pages floor(from_len[b] / 16) .. floor(to_len[b] / 16) - 1 are read
+ * through batch->page_table and written through cache8->page_table: after a
+ * prefill from_len is NULL (zeros) and to_len the prompt lengths; after a
+ * verify step from_len is the old prefix_len and to_len the compaction's
+ * new_len.  Per (page, KV head), of K and of V:
+ *     scale = amax / qmax,  code = round(x * qmax / amax)
+ * with amax = max |x| over the block's 16 x D values, qmax = 448 (e4m3) or
+ * 127 (int8), the quotient taken in fp32 and rounded to nearest, ties to
+ * even; a block of zeros has scale 0 and zero codes.  A block with an
+ * infinity or NaN is written with scale NaN and zero codes, and
+ * JSV_ERR_DEVICE_INPUT goes to dev_status.  Other pages of the 8-bit cache
+ * are left as they are.  Of the batch, B, Hkv, D, num_pages, the page table
+ * and dev_status are used.  A request whose lengths are not
+ * 0 <= from_len <= to_len or need a page past either table's row, or a page
+ * whose entry is out of range, is flagged (JSV_ERR_DEVICE_INPUT) and skipped.
+ * Two requests must not write the same 8-bit page in one call.
+ * Supported: B <= JSV_PAGES_MAX_ROWS.
+ *   from_len, to_len   device [B] int32 (from_len may be NULL)
+ */
+#define JSV_PAGES_MAX_ROWS 8192
+JSV_API jsv_status jsv_kv8_quantize(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *k_cache,
+                                    const uint16_t *v_cache, const int32_t *from_len, const int32_t *to_len,
+                                    void *stream);
+
+/*
+ * Page pool.  The library's calls take page tables as given; these calls
+ * fill and empty them on the device, with no host round trip and in graph
+ * capture.  A pool is num_pages physical pages (of every buffer that shares
+ * the table: the K and V caches of all layers) and one reference count for
+ * each: 0 = free, n = n page-table entries hold it.  The caller zero-fills
+ * refcount once.  A table is [B][max_pages_per_req] int32, -1 = unmapped.
+ * A free page is always taken lowest index first and requests are served in
+ * row order, so the result depends on nothing but the inputs.  Full pages
+ * are never written again, so rows may share them; a partial page is held by
+ * one row.  Calls on one pool are issued on one stream.
+ * Supported: B <= JSV_PAGES_MAX_ROWS; lengths are in slots, at most
+ * 16 * max_pages_per_req (a row outside that is flagged with
+ * JSV_ERR_DEVICE_INPUT and skipped).
+ */
+typedef struct {
+    int32_t num_pages;
+    int32_t *refcount;           /* device [num_pages]                            */
+    int32_t *dev_status;         /* device [1] or NULL: first device-side error   */
+} jsv_page_pool;
+
+/* Bytes of scratch for jsv_pages_alloc, jsv_pages_fork and
+ * jsv_pages_compact on a pool of num_pages pages and tables of B rows or
+ * forks; 16-B aligned, any contents, written and read within the call. */
+JSV_API size_t jsv_pages_workspace_size(int32_t num_pages, int32_t B);
+
+/*
+ * Map fresh pages: every unmapped entry of row b among the logical pages
+ * floor(begin[b] / 16) .. ceil(end[b] / 16) - 1 gets a free page (reference
+ * count 1); with full_only != 0 the range ends at floor(end[b] / 16) (the
+ * pages that end[b] slots fill).  Rows are served in order while the pages
+ * last: a row whose pages do not fit after all that the rows before it ask
+ * for is left as it was and JSV_ERR_NO_PAGES is written to dev_status.
+ *   page_table   device [B][max_pages_per_req], updated
+ *   begin, end   device [B] int32 (begin may be NULL: zeros)
+ */
+JSV_API jsv_status jsv_pages_alloc(const jsv_page_pool *pool, int32_t *page_table, int32_t B,
+                                   int32_t max_pages_per_req, const int32_t *begin, const int32_t *end,
+                                   int32_t full_only, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Fork rows: for i = 0..n-1, row dst[i] becomes a copy of the first len[i]
+ * slots of row src[i].  The floor(len / 16) full pages are shared (unmapped
+ * entries stay unmapped); a partial page gets a fresh page for dst and the
+ * pair goes to copy_src[i], copy_dst[i] for jsv_pages_copy (-1, -1 where
+ * nothing is to be copied).  With full_only != 0 the partial page is left
+ * out (a table of 8-bit pages, which are always full).
+ * Row dst must be wholly unmapped, appear once among dst, and be no fork's
+ * src; else, and where the partial page of src is unmapped or an entry is
+ * out of range or free, fork i is skipped and JSV_ERR_DEVICE_INPUT written
+ * (of forks with the same dst the first is made).  A fork that does not get
+ * its page is skipped with JSV_ERR_NO_PAGES.
+ *   src, dst, len        device [n] int32, 0 <= n <= JSV_PAGES_MAX_ROWS
+ *   copy_src, copy_dst   device [n] int32
+ */
+JSV_API jsv_status jsv_pages_fork(const jsv_page_pool *pool, int32_t *page_table, int32_t B,
+                                  int32_t max_pages_per_req, int32_t n, const int32_t *src, const int32_t *dst,
+                                  const int32_t *len, int32_t full_only, int32_t *copy_src, int32_t *copy_dst,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Free pages: of row b the logical pages floor(keep_begin[b] / 16) ..
+ * ceil(keep_end[b] / 16) - 1 stay; every other mapped entry is unmapped and
+ * its page's reference count falls by one (free at 0).  keep_begin NULL =
+ * zeros: what lies past keep_end goes.  keep_begin = keep_end = new_len
+ * leaves the partial page alone: what a bf16 table keeps once its full pages
+ * are in the 8-bit cache.  keep_end = 0 empties the row.  An entry whose page
+ * is out of range or already free is unmapped and flagged.
+ */
+JSV_API jsv_status jsv_pages_trim(const jsv_page_pool *pool, int32_t *page_table, int32_t B,
+                                  int32_t max_pages_per_req, const int32_t *keep_begin, const int32_t *keep_end,
+                                  void *stream);
+
+/*
+ * Plan a compaction: with U pages in use, every used page at index >= U moves
+ * to a free page below U, both in ascending order, so that the used pages
+ * become 0 .. U-1 (the pool's end can be handed back).  Nothing of the input
+ * changes (page_table may equal new_table): after jsv_pages_copy has moved
+ * the contents, the caller goes on with the new table and counts.
+ *   new_table            device [B][max_pages_per_req] output
+ *   new_refcount         device [num_pages] output
+ *   copy_src, copy_dst   device [max_copies] output, -1 past the last pair
+ *   max_copies           at least num_pages / 2 (the most pages that can move)
+ *   num_copies           device [1] output
+ * A table entry whose page is out of range or free becomes -1 and is flagged.
+ */
+JSV_API jsv_status jsv_pages_compact(const jsv_page_pool *pool, const int32_t *page_table, int32_t B,
+                                     int32_t max_pages_per_req, int32_t *new_table, int32_t *new_refcount,
+                                     int32_t *copy_src, int32_t *copy_dst, int32_t max_copies, int32_t *num_copies,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Copy page contents in every buffer that shares the pool: for each pair
+ * i < n (and < *num_copies where given) with copy_src[i] >= 0, page
+ * copy_src[i] of every buffer is copied to page copy_dst[i].  No destination
+ * may appear twice or be a source (the lists of jsv_pages_fork and
+ * jsv_pages_compact are so).  A pair out of range is flagged and skipped.
+ *   buffers      host array [n_buffers] of device addresses (page 0), read
+ *                before the call returns; 4-B aligned, 16-B aligned copies
+ *                faster
+ *   page_bytes   host array [n_buffers]: bytes of one page, multiples of 4
+ *   copy_src, copy_dst, num_copies   device (num_copies may be NULL)
+ */
+JSV_API jsv_status jsv_pages_copy(const jsv_page_pool *pool, void *const *buffers, const int64_t *page_bytes,
+                                  int32_t n_buffers, const int32_t *copy_src, const int32_t *copy_dst, int32_t n,
+                                  const int32_t *num_copies, void *stream);
 
 /* Number of kernels this library has launched in the calling process since
  * it was loaded (all devices, all streams).  A diagnostic for counting the

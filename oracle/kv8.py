@@ -1,0 +1,104 @@
+"""Oracle of the 8-bit KV cache: codes, quantisation and tree attention over a
+prefix held in 8 bits, in plain fp64 numpy.
+
+TEST INFRASTRUCTURE ONLY, as the rest of this package: nothing here is shared
+with the CUDA path.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from . import bf16_to_f64
+
+PAGE = 16
+QMAX = {"e4m3": 448.0, "int8": 127.0}
+
+
+def decode(codes: np.ndarray, fmt: str) -> np.ndarray:
+    """uint8 codes to the numbers they stand for."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    if fmt == "int8":
+        return np.where(c >= 128, c - 256, c).astype(np.float64)
+    e, m = (c >> 3) & 15, (c & 7).astype(np.float64)
+    mag = np.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * 2.0 ** (e - 7.0))
+    mag = np.where((c & 127) == 127, np.nan, mag)
+    return np.where(c >= 128, -mag, mag)
+
+
+def encode(y: np.ndarray, fmt: str) -> np.ndarray:
+    """Numbers (already divided by their scale) to the nearest codes, ties to
+    even; found by search over all codes of the format."""
+    y = np.asarray(y, dtype=np.float64)
+    if fmt == "int8":
+        return np.rint(y).astype(np.int64).astype(np.uint8)
+    vals = decode(np.arange(127), fmt)                     # 0 .. 448, ascending with the code
+    mag = np.abs(y)
+    hi = np.clip(np.searchsorted(vals, mag), 1, 126)
+    lo = hi - 1
+    dl, dh = mag - vals[lo], vals[hi] - mag
+    code = np.where(dl < dh, lo, np.where(dh < dl, hi, np.where(lo % 2 == 0, lo, hi)))
+    return (code + 128 * np.signbit(y)).astype(np.uint8)
+
+
+def quantize_block(x: np.ndarray, fmt: str):
+    """Codes and fp32 scale of one block of bf16 values (as fp64)."""
+    if not np.isfinite(x).all():
+        return np.zeros(x.shape, np.uint8), np.float32(np.nan)
+    amax = np.abs(x).max()
+    y = x * QMAX[fmt] / (amax if amax > 0 else 1.0)
+    return encode(y, fmt), np.float32(np.float32(amax) / np.float32(QMAX[fmt]))
+
+
+def quantize(k_cache, page_table, page_table8, from_len, to_len, codes, scales, fmt):
+    """In place on ``codes`` [pages][Hkv][16][D] and ``scales``: the full pages
+    of slots [from_len, to_len) of every request."""
+    x = bf16_to_f64(k_cache)
+    for b, (f, t) in enumerate(zip(from_len, to_len)):
+        for lp in range(int(f) // PAGE, int(t) // PAGE):
+            for g in range(x.shape[2]):
+                c, s = quantize_block(x[page_table[b, lp], :, g], fmt)
+                codes[page_table8[b, lp], g], scales[page_table8[b, lp], g] = c, s
+
+
+def tree_attention(case, fmt):
+    """fp64 outputs [T][Hq][D], the average magnitude sum p |v| / sum p of each,
+    each row's largest scale * sum_d |q_d k_d|, and for each output the sum of
+    the 8-bit V codes' magnitudes times the largest V scale, of a case with keys
+    Hq, Hkv, D, prefix_len, node_offsets, parent, page_table, k_cache, v_cache
+    (bf16 bits), page_table8, k8, v8 (codes), k_scale, v_scale, q, scale."""
+    Hq, Hkv, D = case["Hq"], case["Hkv"], case["D"]
+    G, offs = Hq // Hkv, case["node_offsets"]
+    T = int(offs[-1])
+    out, mag, top = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.zeros((T, Hq))
+    codes = np.zeros((T, Hq, D))
+    q = bf16_to_f64(case["q"])
+    kc, vc = bf16_to_f64(case["k_cache"]), bf16_to_f64(case["v_cache"])
+    for b in range(len(offs) - 1):
+        s0, n, P = int(offs[b]), int(offs[b + 1] - offs[b]), int(case["prefix_len"][b])
+        full = P // PAGE
+        pg8 = case["page_table8"][b, :full]
+        slots = np.arange(full * PAGE, P + n)
+        pg = case["page_table"][b][slots // PAGE]
+        sees = np.zeros((n, P + n), dtype=bool)
+        sees[:, :P] = True
+        for i in range(n):
+            j = i
+            while j >= 0:
+                sees[i, P + j] = True
+                j = int(case["parent"][s0 + j])
+        for g in range(Hkv):
+            K, V = [np.concatenate([(decode(case[c][pg8, g], fmt) * case[s][pg8, g].astype(np.float64)[:, None, None])
+                                    .reshape(-1, D), x[pg, slots % PAGE, g]])
+                    for c, s, x in (("k8", "k_scale", kc), ("v8", "v_scale", vc))]
+            codes[s0:s0 + n, g * G:(g + 1) * G] = np.abs(decode(case["v8"][pg8, g], fmt)).sum(axis=(0, 1)) * \
+                case["v_scale"][pg8, g].max(initial=0)
+            for h in range(g * G, (g + 1) * G):
+                for i in range(n):
+                    at = np.flatnonzero(sees[i])
+                    s = case["scale"] * (K[at] @ q[s0 + i, h])
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    out[s0 + i, h] = p @ V[at]
+                    mag[s0 + i, h] = p @ np.abs(V[at])
+                    top[s0 + i, h] = case["scale"] * (np.abs(K[at]) @ np.abs(q[s0 + i, h])).max()
+    return out, mag, top, codes

@@ -23,6 +23,30 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+// What the 8-bit cache's calls use of the structure beside a checked batch.
+jsv_status check_kv8(const jsv_batch *b, const jsv_kv8 *c) {
+    if (!c) return JSV_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->max_pages_per_req < 1) return JSV_ERR_INVALID_ARG;
+    if (c->format != JSV_KV8_E4M3 && c->format != JSV_KV8_INT8) return JSV_ERR_UNSUPPORTED;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table) return JSV_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return JSV_ERR_INVALID_ARG;
+    // rows of the code arrays are 32-bit coordinates of the copies
+    if ((long long)c->num_pages * b->Hkv * 16 > 0x7fffffff) return JSV_ERR_UNSUPPORTED;
+    if ((long long)b->B * b->Hkv > 65535) return JSV_ERR_UNSUPPORTED;    // a grid dimension
+    return JSV_OK;
+}
+
+jsv_status check_pool(const jsv_page_pool *p, const void *table, int32_t B, int32_t max_pages) {
+    if (!p || !p->refcount || !table || p->num_pages < 1 || B < 1 || max_pages < 1) return JSV_ERR_INVALID_ARG;
+    // slot counts of a row are 32-bit
+    if (B > JSV_PAGES_MAX_ROWS || max_pages > 0x7ffffff) return JSV_ERR_UNSUPPORTED;
+    return JSV_OK;
+}
+
+jsv_status check_workspace(const void *ws, size_t have, size_t need) {
+    return have < need || !ws || !aligned(ws, 16) ? JSV_ERR_INVALID_ARG : JSV_OK;
+}
+
 jsv_status check_batch(const jsv_batch *b) {
     if (!b) return JSV_ERR_INVALID_ARG;
     if (b->B < 1 || b->Hq < 1 || b->Hkv < 1 || b->total_nodes < b->B || b->max_nodes < 1 ||
@@ -160,6 +184,112 @@ jsv_status jsv_accum_logp_tree(const float *logp, const int32_t *topk_tokens, co
                                                  static_cast<cudaStream_t>(stream)));
 }
 
+size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, const jsv_kv8 *cache8) {
+    if (check_batch(batch) != JSV_OK || check_kv8(batch, cache8) != JSV_OK) return 0;
+    return jsv::attention_kv8_workspace_bytes(jsv::to_args(batch));
+}
+
+jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
+                                  const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    jsv_status s = check_batch(batch);
+    if (s != JSV_OK) return s;
+    s = check_kv8(batch, cache8);
+    if (s != JSV_OK) return s;
+    if (!q || !k_cache || !v_cache || !out) return JSV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+        return JSV_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > 3.0e38f) return JSV_ERR_INVALID_ARG;
+    const jsv::BatchArgs a = jsv::to_args(batch);
+    const size_t need = jsv::attention_kv8_workspace_bytes(a);
+    if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 256)))) return JSV_ERR_INVALID_ARG;
+    return from_cuda(jsv::launch_tree_attention_kv8(a, *cache8, q, k_cache, v_cache, scale, out, workspace,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
+jsv_status jsv_kv8_quantize(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *k_cache,
+                            const uint16_t *v_cache, const int32_t *from_len, const int32_t *to_len, void *stream) {
+    jsv_status s = check_batch(batch);
+    if (s != JSV_OK) return s;
+    s = check_kv8(batch, cache8);
+    if (s != JSV_OK) return s;
+    if (batch->B > JSV_PAGES_MAX_ROWS || (long long)batch->B * cache8->max_pages_per_req > 0x7fffffff)
+        return JSV_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || !to_len || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return JSV_ERR_INVALID_ARG;
+    return from_cuda(jsv::launch_kv8_quantize(jsv::to_args(batch), *cache8, k_cache, v_cache, from_len, to_len,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+size_t jsv_pages_workspace_size(int32_t num_pages, int32_t B) {
+    if (num_pages < 1 || B < 1) return 0;
+    return jsv::pages_workspace_bytes(num_pages, B);
+}
+
+jsv_status jsv_pages_alloc(const jsv_page_pool *pool, int32_t *page_table, int32_t B, int32_t max_pages_per_req,
+                           const int32_t *begin, const int32_t *end, int32_t full_only, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    jsv_status s = check_pool(pool, page_table, B, max_pages_per_req);
+    if (s != JSV_OK) return s;
+    if (!end) return JSV_ERR_INVALID_ARG;
+    s = check_workspace(workspace, workspace_bytes, jsv::pages_workspace_bytes(pool->num_pages, B));
+    if (s != JSV_OK) return s;
+    return from_cuda(jsv::launch_pages_alloc(*pool, page_table, B, max_pages_per_req, begin, end, full_only != 0,
+                                             workspace, static_cast<cudaStream_t>(stream)));
+}
+
+jsv_status jsv_pages_fork(const jsv_page_pool *pool, int32_t *page_table, int32_t B, int32_t max_pages_per_req,
+                          int32_t n, const int32_t *src, const int32_t *dst, const int32_t *len, int32_t full_only,
+                          int32_t *copy_src, int32_t *copy_dst, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    jsv_status s = check_pool(pool, page_table, B, max_pages_per_req);
+    if (s != JSV_OK) return s;
+    if (n < 0) return JSV_ERR_INVALID_ARG;
+    if (n > JSV_PAGES_MAX_ROWS) return JSV_ERR_UNSUPPORTED;
+    if (n == 0) return JSV_OK;
+    if (!src || !dst || !len || !copy_src || !copy_dst) return JSV_ERR_INVALID_ARG;
+    s = check_workspace(workspace, workspace_bytes, jsv::pages_workspace_bytes(pool->num_pages, n));
+    if (s != JSV_OK) return s;
+    return from_cuda(jsv::launch_pages_fork(*pool, page_table, B, max_pages_per_req, n, src, dst, len, full_only != 0,
+                                            copy_src, copy_dst, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+jsv_status jsv_pages_trim(const jsv_page_pool *pool, int32_t *page_table, int32_t B, int32_t max_pages_per_req,
+                          const int32_t *keep_begin, const int32_t *keep_end, void *stream) {
+    jsv_status s = check_pool(pool, page_table, B, max_pages_per_req);
+    if (s != JSV_OK) return s;
+    if (!keep_end) return JSV_ERR_INVALID_ARG;
+    return from_cuda(jsv::launch_pages_trim(*pool, page_table, B, max_pages_per_req, keep_begin, keep_end,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+jsv_status jsv_pages_compact(const jsv_page_pool *pool, const int32_t *page_table, int32_t B,
+                             int32_t max_pages_per_req, int32_t *new_table, int32_t *new_refcount, int32_t *copy_src,
+                             int32_t *copy_dst, int32_t max_copies, int32_t *num_copies, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    jsv_status s = check_pool(pool, page_table, B, max_pages_per_req);
+    if (s != JSV_OK) return s;
+    if (!new_table || !new_refcount || !num_copies || new_refcount == pool->refcount) return JSV_ERR_INVALID_ARG;
+    if (max_copies < pool->num_pages / 2 || (max_copies > 0 && (!copy_src || !copy_dst))) return JSV_ERR_INVALID_ARG;
+    s = check_workspace(workspace, workspace_bytes, jsv::pages_workspace_bytes(pool->num_pages, B));
+    if (s != JSV_OK) return s;
+    return from_cuda(jsv::launch_pages_compact(*pool, page_table, B, max_pages_per_req, new_table, new_refcount,
+                                               copy_src, copy_dst, max_copies, num_copies, workspace,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+jsv_status jsv_pages_copy(const jsv_page_pool *pool, void *const *buffers, const int64_t *page_bytes,
+                          int32_t n_buffers, const int32_t *copy_src, const int32_t *copy_dst, int32_t n,
+                          const int32_t *num_copies, void *stream) {
+    if (!pool || pool->num_pages < 1 || n_buffers < 0 || n < 0) return JSV_ERR_INVALID_ARG;
+    if (n_buffers == 0 || n == 0) return JSV_OK;
+    if (!buffers || !page_bytes || !copy_src || !copy_dst) return JSV_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n_buffers; ++i)
+        if (!buffers[i] || !aligned(buffers[i], 4) || page_bytes[i] < 4 || page_bytes[i] % 4 != 0)
+            return JSV_ERR_INVALID_ARG;
+    return from_cuda(jsv::launch_pages_copy(*pool, buffers, page_bytes, n_buffers, copy_src, copy_dst, n, num_copies,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
 const char *jsv_status_string(jsv_status status) {
     switch (status) {
         case JSV_OK: return "ok";
@@ -169,11 +299,12 @@ const char *jsv_status_string(jsv_status status) {
         case JSV_ERR_TIMEOUT: return "device wait timed out";
         case JSV_ERR_DEVICE_INPUT: return "malformed device-side input";
         case JSV_ERR_BOUNDS: return "index out of bounds (checked build)";
+        case JSV_ERR_NO_PAGES: return "page pool exhausted";
     }
     return "unknown status";
 }
 
-int32_t jsv_version(void) { return 100; }
+int32_t jsv_version(void) { return 200; }
 
 int32_t jsv_build_flags(void) {
 #ifdef JSV_CHECK_BOUNDS

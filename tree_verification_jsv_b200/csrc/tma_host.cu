@@ -52,6 +52,20 @@ bool encode_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint6
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+    std::call_once(g_once, resolve);
+    if (!g_encode || (inner != 64 && inner != 128)) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {(cuuint32_t)inner, box_outer};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 int device_sm_count() {
     // several host threads may fill an entry at once; they store the same value
     static std::atomic<int> cache[64] = {};

@@ -26,13 +26,22 @@ JSV_ERR_CUDA = 3
 JSV_ERR_TIMEOUT = 4
 JSV_ERR_DEVICE_INPUT = 5
 JSV_ERR_BOUNDS = 6
+JSV_ERR_NO_PAGES = 7
 
 EXPORTS = ("jsv_tree_attention_workspace_size", "jsv_tree_attention",
            "jsv_lmhead_argmax_workspace_size", "jsv_lmhead_argmax", "jsv_accept_path",
            "jsv_kv_compact", "jsv_status_string", "jsv_version", "jsv_kernel_launches",
            "jsv_lmhead_argmax_noalloc", "jsv_last_error_string", "jsv_selftest_wait_timeout",
            "jsv_selftest_lmhead_timeout",
-           "jsv_accum_logp_tree", "jsv_tree_qkv_rope", "jsv_accept_compact", "jsv_build_flags")
+           "jsv_accum_logp_tree", "jsv_tree_qkv_rope", "jsv_accept_compact", "jsv_build_flags",
+           "jsv_tree_attention_kv8_workspace_size", "jsv_tree_attention_kv8", "jsv_kv8_quantize",
+           "jsv_pages_workspace_size", "jsv_pages_alloc", "jsv_pages_fork", "jsv_pages_trim", "jsv_pages_compact",
+           "jsv_pages_copy")
+
+# 8-bit cache formats (jsv_kv8_format) by name, and the most rows of a page
+# table the page-pool calls take (JSV_PAGES_MAX_ROWS).
+KV8_FORMATS = {"e4m3": 0, "int8": 1}
+PAGES_MAX_ROWS = 8192
 
 # Largest node count jsv_lmhead_argmax_noalloc accepts (JSV_NOALLOC_MAX_NODES).
 NOALLOC_MAX_NODES = 8192
@@ -56,6 +65,16 @@ class jsv_batch(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
                 ("node_offsets", ctypes.c_void_p), ("parent", ctypes.c_void_p),
                 ("dev_status", ctypes.c_void_p)]
+
+
+class jsv_kv8(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages_per_req", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class jsv_page_pool(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("refcount", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
 def library_path() -> Path:
@@ -104,6 +123,25 @@ def load() -> ctypes.CDLL:
     lib.jsv_selftest_lmhead_timeout.restype = ctypes.c_int
     lib.jsv_last_error_string.argtypes = []
     lib.jsv_last_error_string.restype = ctypes.c_char_p
+    kp, pp = ctypes.POINTER(jsv_kv8), ctypes.POINTER(jsv_page_pool)
+    lib.jsv_tree_attention_kv8_workspace_size.argtypes = [bp, kp]
+    lib.jsv_tree_attention_kv8_workspace_size.restype = sz
+    lib.jsv_tree_attention_kv8.argtypes = [bp, kp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
+    lib.jsv_tree_attention_kv8.restype = ctypes.c_int
+    lib.jsv_kv8_quantize.argtypes = [bp, kp, vp, vp, vp, vp, vp]
+    lib.jsv_kv8_quantize.restype = ctypes.c_int
+    lib.jsv_pages_workspace_size.argtypes = [i32, i32]
+    lib.jsv_pages_workspace_size.restype = sz
+    lib.jsv_pages_alloc.argtypes = [pp, vp, i32, i32, vp, vp, i32, vp, sz, vp]
+    lib.jsv_pages_alloc.restype = ctypes.c_int
+    lib.jsv_pages_fork.argtypes = [pp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.jsv_pages_fork.restype = ctypes.c_int
+    lib.jsv_pages_trim.argtypes = [pp, vp, i32, i32, vp, vp, vp]
+    lib.jsv_pages_trim.restype = ctypes.c_int
+    lib.jsv_pages_compact.argtypes = [pp, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.jsv_pages_compact.restype = ctypes.c_int
+    lib.jsv_pages_copy.argtypes = [pp, vp, vp, i32, vp, vp, i32, vp, vp]
+    lib.jsv_pages_copy.restype = ctypes.c_int
     lib.jsv_kernel_launches.argtypes = []
     lib.jsv_kernel_launches.restype = ctypes.c_uint64
     _lib = lib
@@ -249,3 +287,84 @@ def jsv_accept_compact(batch, tokens, argmax, max_path, path, accept_len, bonus,
                                    _addr(path), _addr(accept_len), _addr(bonus), _addr(k_cache),
                                    _addr(v_cache), _addr(new_len), _stream(stream))
     _check("jsv_accept_compact", st)
+
+
+def make_kv8(*, format, num_pages, max_pages_per_req, k, v, k_scale, v_scale, page_table) -> jsv_kv8:
+    """The 8-bit cache of ``include/jsv.h``; ``format`` is "e4m3", "int8" or
+    the C value."""
+    return jsv_kv8(int(KV8_FORMATS.get(format, format)), int(num_pages), int(max_pages_per_req), _addr(k), _addr(v),
+                   _addr(k_scale), _addr(v_scale), _addr(page_table))
+
+
+def jsv_tree_attention_kv8_workspace_size(batch: jsv_batch, cache8: jsv_kv8) -> int:
+    return int(load().jsv_tree_attention_kv8_workspace_size(ctypes.byref(batch), ctypes.byref(cache8)))
+
+
+def jsv_tree_attention_kv8(batch, cache8, q, k_cache, v_cache, scale, out, workspace, workspace_bytes=None,
+                           stream=None) -> None:
+    st = load().jsv_tree_attention_kv8(ctypes.byref(batch), ctypes.byref(cache8), _addr(q), _addr(k_cache),
+                                       _addr(v_cache), float(scale), _addr(out), _addr(workspace),
+                                       _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check("jsv_tree_attention_kv8", st)
+
+
+def jsv_kv8_quantize(batch, cache8, k_cache, v_cache, from_len, to_len, stream=None) -> None:
+    st = load().jsv_kv8_quantize(ctypes.byref(batch), ctypes.byref(cache8), _addr(k_cache), _addr(v_cache),
+                                 _addr(from_len), _addr(to_len), _stream(stream))
+    _check("jsv_kv8_quantize", st)
+
+
+def make_page_pool(*, num_pages, refcount, dev_status=None) -> jsv_page_pool:
+    return jsv_page_pool(int(num_pages), _addr(refcount), _addr(dev_status))
+
+
+def make_page_buffers(buffers, page_bytes):
+    """Host arrays of buffer addresses and page sizes for ``jsv_pages_copy``;
+    holds on to the tensors."""
+    n = len(buffers)
+    return ((ctypes.c_void_p * n)(*[_addr(x) for x in buffers]),
+            (ctypes.c_int64 * n)(*[int(x) for x in page_bytes]), n, list(buffers))
+
+
+def jsv_pages_workspace_size(num_pages, B) -> int:
+    return int(load().jsv_pages_workspace_size(int(num_pages), int(B)))
+
+
+def jsv_pages_alloc(pool, page_table, B, max_pages_per_req, begin, end, full_only, workspace, workspace_bytes=None,
+                    stream=None) -> None:
+    st = load().jsv_pages_alloc(ctypes.byref(pool), _addr(page_table), int(B), int(max_pages_per_req), _addr(begin),
+                                _addr(end), int(bool(full_only)), _addr(workspace),
+                                _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check("jsv_pages_alloc", st)
+
+
+def jsv_pages_fork(pool, page_table, B, max_pages_per_req, n, src, dst, length, full_only, copy_src, copy_dst,
+                   workspace, workspace_bytes=None, stream=None) -> None:
+    st = load().jsv_pages_fork(ctypes.byref(pool), _addr(page_table), int(B), int(max_pages_per_req), int(n),
+                               _addr(src), _addr(dst), _addr(length), int(bool(full_only)), _addr(copy_src),
+                               _addr(copy_dst), _addr(workspace), _nbytes(workspace, workspace_bytes),
+                               _stream(stream))
+    _check("jsv_pages_fork", st)
+
+
+def jsv_pages_trim(pool, page_table, B, max_pages_per_req, keep_begin, keep_end, stream=None) -> None:
+    st = load().jsv_pages_trim(ctypes.byref(pool), _addr(page_table), int(B), int(max_pages_per_req),
+                               _addr(keep_begin), _addr(keep_end), _stream(stream))
+    _check("jsv_pages_trim", st)
+
+
+def jsv_pages_compact(pool, page_table, B, max_pages_per_req, new_table, new_refcount, copy_src, copy_dst, max_copies,
+                      num_copies, workspace, workspace_bytes=None, stream=None) -> None:
+    st = load().jsv_pages_compact(ctypes.byref(pool), _addr(page_table), int(B), int(max_pages_per_req),
+                                  _addr(new_table), _addr(new_refcount), _addr(copy_src), _addr(copy_dst),
+                                  int(max_copies), _addr(num_copies), _addr(workspace),
+                                  _nbytes(workspace, workspace_bytes), _stream(stream))
+    _check("jsv_pages_compact", st)
+
+
+def jsv_pages_copy(pool, buffers, copy_src, copy_dst, n, num_copies=None, stream=None) -> None:
+    """``buffers``: what ``make_page_buffers`` returned."""
+    addrs, nbytes, n_buffers, _ = buffers
+    st = load().jsv_pages_copy(ctypes.byref(pool), addrs, nbytes, n_buffers, _addr(copy_src), _addr(copy_dst), int(n),
+                               _addr(num_copies), _stream(stream))
+    _check("jsv_pages_copy", st)
