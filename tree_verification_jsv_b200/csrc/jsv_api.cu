@@ -1,6 +1,7 @@
 // C ABI of libjsv.so: host-side argument checks, then one launch sequence
 // per call on the caller's stream.  See include/jsv.h for the contract.
 #include "jsv_internal.cuh"
+#include "kv_internal.cuh"
 
 #include <atomic>
 #include <cstdio>

@@ -231,25 +231,4 @@ cudaError_t launch_accum_logp_tree(const float *logp, const int32_t *topk_tokens
 cudaError_t launch_tree_attention(const BatchArgs &a, const uint16_t *q, const uint16_t *k_cache,
                                   const uint16_t *v_cache, float scale, uint16_t *out, void *ws,
                                   cudaStream_t st);
-size_t attention_kv8_workspace_bytes(const BatchArgs &a);
-cudaError_t launch_tree_attention_kv8(const BatchArgs &a, const jsv_kv8 &c, const uint16_t *q,
-                                      const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,
-                                      void *ws, cudaStream_t st);
-cudaError_t launch_kv8_quantize(const BatchArgs &a, const jsv_kv8 &c, const uint16_t *k_cache,
-                                const uint16_t *v_cache, const int32_t *from_len, const int32_t *to_len,
-                                cudaStream_t st);
-size_t pages_workspace_bytes(int num_pages, int rows);
-cudaError_t launch_pages_alloc(const jsv_page_pool &pool, int32_t *table, int B, int max_pages, const int32_t *begin,
-                               const int32_t *end, bool full_only, void *ws, cudaStream_t st);
-cudaError_t launch_pages_fork(const jsv_page_pool &pool, int32_t *table, int B, int max_pages, int n,
-                              const int32_t *src, const int32_t *dst, const int32_t *len, bool full_only,
-                              int32_t *copy_src, int32_t *copy_dst, void *ws, cudaStream_t st);
-cudaError_t launch_pages_trim(const jsv_page_pool &pool, int32_t *table, int B, int max_pages,
-                              const int32_t *keep_begin, const int32_t *keep_end, cudaStream_t st);
-cudaError_t launch_pages_compact(const jsv_page_pool &pool, const int32_t *table, int B, int max_pages,
-                                 int32_t *new_table, int32_t *new_refcount, int32_t *copy_src, int32_t *copy_dst,
-                                 int max_copies, int32_t *num_copies, void *ws, cudaStream_t st);
-cudaError_t launch_pages_copy(const jsv_page_pool &pool, void *const *buffers, const int64_t *page_bytes,
-                              int n_buffers, const int32_t *copy_src, const int32_t *copy_dst, int n,
-                              const int32_t *num_copies, cudaStream_t st);
 }  // namespace jsv

@@ -16,6 +16,7 @@
 // 1 out a value) and by launch latency after a verify step, where a request
 // completes a page or none.
 #include "jsv_internal.cuh"
+#include "kv_internal.cuh"
 #include "sm100.cuh"
 
 #include <cuda_fp8.h>

@@ -16,6 +16,7 @@
 // latency: two or three rounds of dependent loads and as many barriers.
 // Trimming and copying need no order between CTAs and use plain grids.
 #include "jsv_internal.cuh"
+#include "kv_internal.cuh"
 #include "sm100.cuh"
 
 #include <algorithm>

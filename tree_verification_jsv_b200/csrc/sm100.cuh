@@ -427,8 +427,6 @@ bool encode_tensor_map_2d(CUtensorMap *map, const void *base, uint64_t inner, ui
 bool encode_tensor_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                           uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
                           uint32_t box2);
-// Rows of 64 or 128 bytes, contiguous, swizzled by the row's width.
-bool encode_tensor_map_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer);
 int device_sm_count();
 
 }  // namespace jsv

@@ -1,6 +1,7 @@
 // Host helpers for TMA: tensor-map encoding through the driver entry point
 // (resolved once with cudaGetDriverEntryPoint, so the library does not link
 // libcuda directly) and a per-device SM count cache.
+#include "kv_internal.cuh"
 #include "sm100.cuh"
 
 #include <cudaTypedefs.h>

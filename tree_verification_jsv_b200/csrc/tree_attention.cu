@@ -45,6 +45,7 @@
 // TMEM columns: S/P of group 0 [0,128), of group 1 [128,256); O of group 0
 // [256, 256+D), of group 1 [256+D, 256+2D).
 // Shared memory: Q (2 groups x 16 KB per 64 dims), 2 x (K, V) stages.
+#include "attn_math.cuh"
 #include "jsv_internal.cuh"
 #include "sm100.cuh"
 
@@ -70,43 +71,6 @@ constexpr int kKeyTile = 128;
 constexpr int kStages = 2;
 constexpr int kMaxTreeWords = 16;          // 512 nodes
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&v);
-}
-
-// Packed fp32 pairs (sm_100 f32x2 arithmetic: one instruction per pair).
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 
 struct AttnParams {
     BatchArgs a;
@@ -211,12 +175,6 @@ struct AttnSmem {
     static constexpr int kStageBytes = 2 * kKVBytes;
     static constexpr int kTotal = kQBytes + kStages * kStageBytes;
 };
-
-// Byte offset of 16-byte chunk `c` of row `r` in a K-major SW128 operand
-// region (rows of 128 B, 8-row atoms; chunk index XOR row % 8).
-__device__ __forceinline__ uint32_t sw128_offset(int r, int c) {
-    return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
-}
 
 // The MMA issuer: one thread of the CTA issues every tcgen05.mma.  S of a
 // group reuses the TMEM of that group's previous P; the PV that reads it was

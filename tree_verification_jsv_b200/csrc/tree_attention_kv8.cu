@@ -19,6 +19,7 @@
 // maximum m moves only when a score passes it by 8 (2^8), so most pages need
 // no reduction over the row.
 #include "jsv_internal.cuh"
+#include "kv_internal.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
