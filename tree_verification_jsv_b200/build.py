@@ -15,7 +15,7 @@ SO = PKG / "libjsv.so"
 SO_CHECKED = PKG / "libjsv_checked.so"
 SOURCES = ["jsv_api.cu", "tree_attention.cu", "lmhead_argmax.cu", "accept_path.cu", "kv_compact.cu",
            "lmhead_noalloc.cu", "tma_host.cu", "selftest.cu",
-           "tree_build.cu", "qkv_rope.cu", "tree_attention_kv8.cu", "kv8_quantize.cu", "kv_pages.cu"]
+           "tree_build.cu", "qkv_rope.cu", "tree_attention_kv8.cu", "tree_attention_kv8_tiles.cu", "kv8_quantize.cu", "kv_pages.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

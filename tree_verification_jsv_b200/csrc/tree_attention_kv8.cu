@@ -18,11 +18,7 @@
 // accumulator is rescaled when a page's scale passes 2 vref.  The running
 // maximum m moves only when a score passes it by 8 (2^8), so most pages need
 // no reduction over the row.
-#include "jsv_internal.cuh"
-#include "kv_internal.cuh"
-#include "sm100.cuh"
-
-#include <math.h>
+#include "kv8_attention.cuh"
 
 #include <algorithm>
 
@@ -31,70 +27,6 @@ namespace jsv {
 using namespace sm100;
 
 namespace {
-
-constexpr int kMaxTreeNodes = 512;
-constexpr int kTreeWords = kMaxTreeNodes / 32;
-constexpr float kMaxSlack = 8.f;             // log2 units a score may pass the running maximum by
-constexpr float kWeightShift = 64.f;         // 2^6, see above
-constexpr int kMaxSplits = 64;
-
-struct Kv8Params {
-    BatchArgs a;
-    jsv_kv8 c;
-    const uint16_t *q, *k, *v;
-    uint16_t *out;
-    float scale_log2;
-    int S, C;                                // most splits of a request, pages a split aims at
-    float *ws_o, *ws_ml;                     // [S][T*Hq][D], [S][T*Hq][2]
-};
-
-// The request's descriptors, with the 8-bit table's row checked too.
-__device__ __forceinline__ bool load_request_kv8(const Kv8Params &p, int b, Request &r) {
-    if (!load_request(p.a, b, r)) return false;
-    if (r.P / 16 > p.c.max_pages_per_req) {
-        flag_error(p.a.dev_status, JSV_ERR_DEVICE_INPUT);
-        return false;
-    }
-    return true;
-}
-
-__device__ __forceinline__ int request_pages(const Request &r) { return (r.P + r.n + 15) / 16; }
-__device__ __forceinline__ int page_splits(int pages, int C, int S) { return max(1, min(S, (pages + C - 1) / C)); }
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp16 from two fp32, the first in the low half.
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Four codes to fp16, exactly.  An int8 code u - 128 comes from the fp16
-// number 1024 + u, whose low byte is u.
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (FMT == JSV_KV8_E4M3) {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(l), "r"(0x64806480u));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(0x64806480u));
-    }
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -172,7 +104,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int rows_total = r.n * G;
     if (m0 >= rows_total) return;
     const int pages = request_pages(r), pages8 = r.P / 16;
-    const int Sb = page_splits(pages, p.C, p.S);
+    const int Sb = unit_splits(pages, p.C, p.S);
     if (split >= Sb) return;
     const int t0 = (int)((long long)pages * split / Sb), t1 = (int)((long long)pages * (split + 1) / Sb);
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
@@ -330,7 +262,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     if (mx > m[mt][hh] + kMaxSlack) {
-                        const float corr = exp2_fast(m[mt][hh] - mx);        // 0 from -inf
+                        const float corr = fast_exp2(m[mt][hh] - mx);        // 0 from -inf
                         scale_o(mt, hh, corr);
                         l[mt][hh] *= corr;
                         m[mt][hh] = mx;
@@ -346,7 +278,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int k = 2 * hh; k < 2 * hh + 2; ++k) {
-                        sc[mt][j][k] = exp2_fast(sc[mt][j][k] - base);
+                        sc[mt][j][k] = fast_exp2(sc[mt][j][k] - base);
                         l[mt][hh] += sc[mt][j][k];
                     }
             }
@@ -551,10 +483,10 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             uint32_t pa[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                pa[mt][0] = pack_bf16(sc[mt][0][0] * pv, sc[mt][0][1] * pv);
-                pa[mt][1] = pack_bf16(sc[mt][0][2] * pv, sc[mt][0][3] * pv);
-                pa[mt][2] = pack_bf16(sc[mt][1][0] * pv, sc[mt][1][1] * pv);
-                pa[mt][3] = pack_bf16(sc[mt][1][2] * pv, sc[mt][1][3] * pv);
+                pa[mt][0] = pack_bf16x2(sc[mt][0][0] * pv, sc[mt][0][1] * pv);
+                pa[mt][1] = pack_bf16x2(sc[mt][0][2] * pv, sc[mt][0][3] * pv);
+                pa[mt][2] = pack_bf16x2(sc[mt][1][0] * pv, sc[mt][1][1] * pv);
+                pa[mt][3] = pack_bf16x2(sc[mt][1][2] * pv, sc[mt][1][3] * pv);
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -609,7 +541,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int w = 0; w < kRowWarps; ++w) {
             const float mw = m_sh[w][row], lw = l_sh[w][row];
             if (mw == -INFINITY && lw == 0.f) continue;          // saw nothing
-            const float f = mw == -INFINITY ? 1.f : exp2_fast(mw - M);
+            const float f = mw == -INFINITY ? 1.f : fast_exp2(mw - M);
             const float4 v = *reinterpret_cast<const float4 *>(smem + w * L::kWarp + (row * D + 4 * c) * 4);
             acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
@@ -620,8 +552,8 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
             const size_t oi = row_id * D + 4 * c;
             if (JSV_IN_BOUNDS(oi + 3, (long long)rows * D, a.dev_status))
-                *reinterpret_cast<uint2 *>(p.out + oi) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
-                                                                    pack_bf16(acc.z * inv, acc.w * inv));
+                *reinterpret_cast<uint2 *>(p.out + oi) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                                    pack_bf16x2(acc.z * inv, acc.w * inv));
         } else {
             const size_t part = (size_t)split * rows + row_id;
             if (JSV_IN_BOUNDS(part, (long long)p.S * rows, a.dev_status)) {
@@ -648,7 +580,7 @@ kv8_merge_kernel(const Kv8Params p) {
     const int rg = blockIdx.x * kMergeWarps + warp;
     Request r;
     if (!load_request_kv8(p, b, r) || rg >= r.n * G) return;
-    const int S = page_splits(request_pages(r), p.C, p.S);
+    const int S = unit_splits(request_units(p, r), p.C, p.S);
     if (S == 1) return;                          // written by the attention kernel
     const size_t rows = (size_t)a.total_nodes * a.Hq;
     const size_t row_id = (size_t)(r.base + rg / G) * a.Hq + g * G + rg % G;
@@ -672,7 +604,7 @@ kv8_merge_kernel(const Kv8Params p) {
     float f[2], lsum = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        f[k] = ls[k] == 0.f ? 0.f : ms[k] == -INFINITY ? 1.f : exp2_fast(ms[k] - M);
+        f[k] = ls[k] == 0.f ? 0.f : ms[k] == -INFINITY ? 1.f : fast_exp2(ms[k] - M);
         lsum = fmaf(f[k], ls[k], lsum);
     }
 #pragma unroll
@@ -695,7 +627,7 @@ kv8_merge_kernel(const Kv8Params p) {
     const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
     uint32_t *out = reinterpret_cast<uint32_t *>(p.out + row_id * D + lane * kPer);
 #pragma unroll
-    for (int x = 0; x < kPer; x += 2) out[x / 2] = pack_bf16(o[x] * inv, o[x + 1] * inv);
+    for (int x = 0; x < kPer; x += 2) out[x / 2] = pack_bf16x2(o[x] * inv, o[x + 1] * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -703,29 +635,49 @@ kv8_merge_kernel(const Kv8Params p) {
 // ---------------------------------------------------------------------------
 namespace {
 
+// Query rows of a KV head (nodes * Hq / Hkv) up to which the page-streaming
+// form is taken.
+constexpr int kRowsFormMost = 32;
+
 struct Kv8Plan {
-    int mt, S, C;
+    int mt;                                      // row tiles of a warp, 0: the tcgen05 form
+    int S, C;
 };
+
+// Splits that minimise waves * (fixed + units of a split) + what a split's
+// partial costs, in units' times; the estimate takes every request for the
+// largest the batch may hold.
+void choose_splits(Kv8Plan &pl, long long units_of_work, int total, int most, int slots, int per_unit, double fixed,
+                   double merge, double per_split) {
+    double best = 1e300;
+    pl.S = 1;
+    for (int s = 1; s <= kMaxSplits && s <= most; ++s) {
+        const long long waves = (units_of_work * s + slots - 1) / slots;
+        const double cost = (double)waves * (fixed + (double)((total + s * per_unit - 1) / (s * per_unit))) +
+                            (s > 1 ? merge + per_split * s : 0.0);
+        if (cost < best - 1e-9) best = cost, pl.S = s;
+    }
+    pl.C = (total + pl.S - 1) / pl.S;
+}
 
 Kv8Plan plan_of(const BatchArgs &a) {
     Kv8Plan pl;
     const int rows = a.max_nodes * (a.Hq / a.Hkv);
-    pl.mt = rows <= 16 ? 1 : 2;
-    const int tiles = (rows + 16 * pl.mt - 1) / (16 * pl.mt);
-    const long long units = (long long)a.B * a.Hkv * tiles;
-    const int total = std::max((a.max_prefix + a.max_nodes + 15) / 16, 1);
-    // Splits that minimise waves * (fixed + pages a warp reads), in units of
-    // a page's time in a warp; resident CTAs an SM as the registers allow.
-    const int slots = std::max(device_sm_count(), 1) * (pl.mt == 1 ? 3 : 2);
-    const double fixed = 8.0;
-    double best = 1e300;
-    pl.S = 1;
-    for (int s = 1; s <= kMaxSplits && s <= std::max(total / kRowWarps, 1); ++s) {
-        const long long waves = (units * s + slots - 1) / slots;
-        const double cost = (double)waves * (fixed + (double)total / (s * kRowWarps)) + (s > 1 ? 4.0 + 0.05 * s : 0.0);
-        if (cost < best) best = cost, pl.S = s;
+    const int sms = std::max(device_sm_count(), 1);
+    if (rows <= kRowsFormMost) {
+        pl.mt = rows <= 16 ? 1 : 2;
+        const int tiles = (rows + 16 * pl.mt - 1) / (16 * pl.mt);
+        const int total = (int)(((long long)a.max_prefix + a.max_nodes + 15) / 16);
+        choose_splits(pl, (long long)a.B * a.Hkv * tiles, total, std::max(total / kRowWarps, 1),
+                      sms * (pl.mt == 1 ? 3 : 2), kRowWarps, 8.0, 4.0, 0.05);
+    } else {
+        pl.mt = 0;
+        const int tiles = (rows + 255) / 256;
+        const int total = (int)(((long long)a.max_prefix / 16 + 7) / 8) + (15 + a.max_nodes + 127) / 128;
+        // a tile takes about 2.1 us; a split's fp32 partial is written and read at about 6 TB/s
+        const double per_split = (double)a.total_nodes * a.Hq * (a.D + 2) * 8.0 / 6.0e6 / 2.1;
+        choose_splits(pl, (long long)a.B * a.Hkv * tiles, total, total, sms, 1, 3.0, 1.0, per_split);
     }
-    pl.C = (total + pl.S - 1) / pl.S;
     return pl;
 }
 
@@ -756,7 +708,9 @@ cudaError_t launch_rows(const Kv8Params &p, cudaStream_t st) {
 template <int D>
 cudaError_t launch_kv8(const Kv8Params &p, int mt, cudaStream_t st) {
     cudaError_t e;
-    if (p.c.format == JSV_KV8_E4M3)
+    if (mt == 0)
+        e = launch_kv8_tiles(p, st);
+    else if (p.c.format == JSV_KV8_E4M3)
         e = mt == 1 ? launch_rows<D, JSV_KV8_E4M3, 1>(p, st) : launch_rows<D, JSV_KV8_E4M3, 2>(p, st);
     else
         e = mt == 1 ? launch_rows<D, JSV_KV8_INT8, 1>(p, st) : launch_rows<D, JSV_KV8_INT8, 2>(p, st);
@@ -792,6 +746,7 @@ cudaError_t launch_tree_attention_kv8(const BatchArgs &a, const jsv_kv8 &c, cons
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = pl.S;
     p.C = pl.C;
+    p.by_tiles = pl.mt == 0;
     p.ws_o = pl.S > 1 ? static_cast<float *>(ws) : nullptr;
     p.ws_ml = pl.S > 1 ? p.ws_o + (size_t)pl.S * a.total_nodes * a.Hq * a.D : nullptr;
     return a.D == 128 ? launch_kv8<128>(p, pl.mt, st) : launch_kv8<64>(p, pl.mt, st);

@@ -1,0 +1,764 @@
+// Tree-causal attention over a prefix held in 8 bits: the form for many query
+// rows, on tcgen05 tensor cores (the arithmetic is described at the head of
+// tree_attention_kv8.cu).
+//
+// One CTA per (request, KV head, 256 packed query rows, split); the rows form
+// two 128-row groups that take turns on the tensor core, as in
+// tree_attention.cu, whose MMA order and softmax this kernel keeps.  What
+// differs is where the operands come from: the codes are read by ordinary
+// 16-byte loads and written to the operand tiles as fp16 by four converting
+// warps, one 128-key tile ahead, so the tensor core, the softmax and the
+// conversion run side by side.
+//
+// Tiles: eight 8-bit pages each (128 keys), then 128-slot tiles of the bf16
+// cache from the first slot past the full pages, copied unconverted and
+// multiplied as bf16: a group's warps put their rows of Q back as bf16 when
+// they hand over the last 8-bit tile's weights.
+//
+//   warps 0..3    codes -> fp16 tiles, scales; bf16 tiles
+//   warp 4        TMEM, MMA issue (one thread); 5..7 idle
+//   warps 8..15   softmax, one query row per thread
+//
+// The K scale of a page multiplies its 16 score columns (it rides on the
+// multiply that brings scores to log2 units).  The V scale goes into the
+// fp16 V tile as vs / vref, a rounding of 2^-10 of each value, instead of
+// into the weights: the converting warps have the instructions to spare, the
+// softmax warps do not.  vref is the CTA's reference scale; it changes only
+// when a page's scale passes 2 vref, and then O is rescaled with the running
+// maximum's correction.
+#include "kv8_attention.cuh"
+
+#include <string.h>
+
+#include <type_traits>
+
+namespace jsv {
+
+namespace {
+
+constexpr int kGroups = 2;
+constexpr int kGroupRows = 128;
+constexpr int kRowsPerCta = kGroups * kGroupRows;
+constexpr int kTileKeys = 128;
+constexpr int kTilePages = kTileKeys / 16;
+constexpr int kStages = 2;
+constexpr int kConvThreads = 128;
+constexpr int kMmaWarp = 4;
+constexpr int kSoftmaxWarp0 = 8;
+constexpr int kTileThreads = 512;
+// registers a thread after the split, of 128 at launch: 112 + 48 + 2 * 176 =
+// 4 * 128 over the four warpgroups
+constexpr int kRegsConv = 112;
+constexpr int kRegsMma = 48;
+constexpr int kRegsSoftmax = 176;
+constexpr int kSlots = 4;                        // tiles whose scales are held, see TileInfo
+constexpr float kWeightLog2 = 6.f;               // weights are held as 2^6 e: e <= 2^8 stays inside fp16
+
+// What the softmax warps need of a tile.  Written before the tile's K is
+// handed over; the slot of tile j is rewritten for tile j + 4, whose K tile
+// cannot start before every softmax warp is past tile j.
+struct __align__(16) TileInfo {
+    float ks[kTilePages];                        // read as two float4
+    float vref, vratio;                          // reference scale, and the previous one over it
+    // bf16 slots whose V row is not finite, as each converting warp found them
+    uint32_t bad[kConvThreads / 32][kTileKeys / 32];
+};
+
+template <int D>
+struct TileSmem {
+    static constexpr int kQGroup = kGroupRows * D * 2;
+    static constexpr int kQ = kGroups * kQGroup;
+    static constexpr int kKV = kTileKeys * D * 2;              // one K (or V) tile
+    static constexpr int kStage = 2 * kKV;
+    static constexpr int kTotal = kQ + kStages * kStage + 1024;
+};
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The MMA issuer, one thread; see attention_mma_loop in tree_attention.cu for
+// the order and for why everything is a constant offset from a base.  Tiles
+// before `n_pre` are fp16, the others bf16.
+template <int D, int NG>
+__device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_t aKV, int ntiles, int n_pre,
+                                             uint64_t *k_full, uint64_t *v_full, uint64_t *k_empty, uint64_t *v_empty,
+                                             uint64_t *s_full, uint64_t *p_full, uint64_t *o_done, uint64_t *q_ready,
+                                             uint64_t *drain_bar, volatile int *abort_sh, int32_t *dev_status) {
+    using L = TileSmem<D>;
+    constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);             // operand types of the descriptor: 0 = fp16
+    constexpr uint32_t id_s = idesc_bf16_f32(128, kTileKeys, false, false) & ~kBf16;
+    constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true) & ~kBf16;
+    constexpr uint32_t kStageStep = L::kStage >> 4;
+    uint64_t dQ = desc_kmajor_sw128(aQ);
+    uint64_t dK0 = desc_kmajor_sw128(aKV);
+    uint64_t dV0 = desc_mnmajor_sw128(aKV + L::kKV, kTileKeys * 128, 1024);
+    auto issue_s = [&](auto grp_c, uint64_t dk, uint32_t type) {
+        constexpr int grp = decltype(grp_c)::value;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = grp * L::kQGroup + (kk >> 2) * (kGroupRows * 128) + (kk & 3) * 32;
+            const uint32_t offk = (kk >> 2) * (kTileKeys * 128) + (kk & 3) * 32;
+            mma_bf16_ss(tmem + grp * 128, dQ + (off >> 4), dk + (offk >> 4), id_s | type, kk > 0);
+        }
+        mma_commit(&s_full[grp]);
+    };
+    auto issue_pv = [&](auto grp_c, uint64_t dv, uint32_t acc_first, uint32_t type) {
+        constexpr int grp = decltype(grp_c)::value;
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+            mma_bf16_ts(tmem + 256 + grp * D, tmem + grp * 128 + kk * 8, dv + ((kk * 2048) >> 4), id_o | type,
+                        kk > 0 ? 1u : acc_first);
+        mma_commit(&o_done[grp]);
+    };
+    using G0 = std::integral_constant<int, 0>;
+    using G1 = std::integral_constant<int, 1>;
+    bool ok = mbar_wait(q_ready, 0, abort_sh);
+    if (ok) ok = mbar_wait(&k_full[0], 0, abort_sh);
+    if (ok) {
+        tc_fence_after();
+        const uint32_t type = n_pre > 0 ? 0u : kBf16;
+        issue_s(G0{}, dK0, type);
+        if constexpr (NG > 1) issue_s(G1{}, dK0, type);
+        mma_commit(&k_empty[0]);
+    }
+    for (int j = 0; ok && j < ntiles; ++j) {
+        asm volatile("" : "+l"(dQ), "+l"(dK0), "+l"(dV0));
+        const int st = j % kStages, stn = (j + 1) % kStages;
+        const uint32_t ph = (uint32_t)((j / kStages) & 1), phn = (uint32_t)(((j + 1) / kStages) & 1);
+        const bool more = j + 1 < ntiles;
+        const uint64_t dv = dV0 + st * kStageStep, dkn = dK0 + stn * kStageStep;
+        const uint32_t acc_first = j > 0 ? 1u : 0u;
+        const uint32_t type = j < n_pre ? 0u : kBf16, type_n = j + 1 < n_pre ? 0u : kBf16;
+        ok = mbar_wait(&v_full[st], ph, abort_sh) && (!more || mbar_wait(&k_full[stn], phn, abort_sh));
+        if (!ok) break;
+        ok = mbar_wait(&p_full[0], j & 1, abort_sh);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(G0{}, dv, acc_first, type);
+        if constexpr (NG == 1) mma_commit(&v_empty[st]);
+        if (more) {
+            issue_s(G0{}, dkn, type_n);
+            if constexpr (NG == 1) mma_commit(&k_empty[stn]);
+        }
+        if constexpr (NG > 1) {
+            ok = mbar_wait(&p_full[1], j & 1, abort_sh);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(G1{}, dv, acc_first, type);
+            mma_commit(&v_empty[st]);
+            if (more) {
+                issue_s(G1{}, dkn, type_n);
+                mma_commit(&k_empty[stn]);
+            }
+        }
+    }
+    if (!ok) {
+        *abort_sh = 1;
+        flag_error(dev_status, JSV_ERR_TIMEOUT);
+    }
+    int zero = 0;
+    mma_commit(drain_bar);
+    mbar_wait(drain_bar, 0, (volatile int *)&zero);
+}
+
+}  // namespace
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+kv8_tiles_kernel(const Kv8Params p) {
+    pdl_allow_dependents();
+    pdl_wait_predecessor();
+    using L = TileSmem<D>;
+    extern __shared__ uint8_t dsmem[];
+    __shared__ __align__(8) uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
+    __shared__ __align__(8) uint64_t s_full[kGroups], p_full[kGroups], o_done[kGroups], q_ready, drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ volatile int abort_sh;
+    __shared__ TileInfo info[kSlots];
+    __shared__ float row_fac[kRowsPerCta];
+    __shared__ uint32_t anc[kRowsPerCta][kTreeWords];
+    __shared__ int par_sh[kMaxTreeNodes];
+
+    const BatchArgs &a = p.a;
+    const int G = a.Hq / a.Hkv;
+    const int b = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv, split = blockIdx.y;
+    const int m0 = blockIdx.x * kRowsPerCta;
+    Request r;
+    if (!load_request_kv8(p, b, r)) return;
+    const int rows_total = r.n * G;
+    if (m0 >= rows_total) return;
+    const int rows_here = min(kRowsPerCta, rows_total - m0);
+    const int ngroups = rows_here > kGroupRows ? 2 : 1;
+
+    // this split's tiles: n_pre of codes, then bf16 ones
+    const int pre_tiles = prefix_tiles(r), total = request_units(p, r), pages8 = r.P / 16;
+    const int Sb = unit_splits(total, p.C, p.S);
+    if (split >= Sb) return;
+    const int t_begin = (int)((long long)total * split / Sb), t_end = (int)((long long)total * (split + 1) / Sb);
+    const int ntiles = t_end - t_begin;
+    const int n_pre = max(0, min(t_end, pre_tiles) - t_begin);
+    const bool has_tail = n_pre < ntiles;
+    const int P0 = pages8 * 16;                  // first slot of the bf16 tiles
+    auto tail_slot = [&](int j) { return P0 + (t_begin + j - pre_tiles) * kTileKeys; };
+
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sKV = smem + L::kQ;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&k_full[s], kConvThreads / 32);
+            mbar_init(&v_full[s], kConvThreads / 32);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int s = 0; s < kGroups; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+            mbar_init(&o_done[s], 1);
+        }
+        mbar_init(&q_ready, 4 * kGroups);
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    if (warp < kConvThreads / 32) {
+        setmaxnreg_dec<kRegsConv>();
+        // ------------------------------------------------------- conversion
+        // A tile's codes are eight contiguous blocks of 16 * D bytes.  A warp's
+        // lanes take 16-byte chunks so that eight neighbouring lanes store to
+        // two rows with an even and an odd number: their swizzled 16-byte
+        // columns then cover all 32 banks.
+        constexpr int kRowChunks = D / 16;                   // 16-byte chunks of codes in a row
+        constexpr int kIters = kTileKeys * kRowChunks / kConvThreads;
+        constexpr int kIterRows = kTileKeys / kIters;        // rows of one iteration: 16 or 32
+        const int crow = D == 128 ? warp * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1) : warp * 8 + (lane >> 2);
+        const int cc = D == 128 ? (lane & 3) | (((lane >> 3) & 1) << 2) : lane & 3;
+        const uint32_t code_off = (crow % 16) * D + cc * 16;
+        // byte offset of this thread's 32 bytes of row crow, first half
+        const uint32_t dst_half = (cc >> 2) * (kTileKeys * 128);
+        const int chunk0 = (cc & 3) * 2;
+        const long long code_bytes = (long long)p.c.num_pages * a.Hkv * 16 * D;
+
+        // lane l < 8: page l of a tile (-1: reads zeros)
+        auto load_pages = [&](int j) -> int {
+            int page = -1;
+            const int lp = (t_begin + j) * kTilePages + lane;
+            if (lane < kTilePages && j < n_pre && lp < pages8) {
+                const long long pi = (long long)b * p.c.max_pages_per_req + lp;
+                if (JSV_IN_BOUNDS(pi, (long long)a.B * p.c.max_pages_per_req, a.dev_status)) page = __ldg(p.c.page_table + pi);
+                if (page < 0 || page >= p.c.num_pages) {
+                    if (warp == 0) flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        auto load_codes = [&](const uint8_t *codes, int pages, uint4 (&w)[kIters]) {
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const int page = __shfl_sync(0xffffffffu, pages, i * (kIterRows / 16) + crow / 16);
+                const size_t at = ((size_t)page * a.Hkv + g) * 16 * D + code_off;
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (page >= 0 && JSV_IN_BOUNDS(at + 15, code_bytes, a.dev_status))
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + at));
+            }
+        };
+        auto store_codes = [&](uint8_t *tile, const uint4 (&w)[kIters], bool scaled, uint32_t ratios) {
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t f[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) codes_to_f16<FMT>(in[k], f[2 * k], f[2 * k + 1]);
+                if (scaled) {
+                    const uint32_t ratio = __shfl_sync(0xffffffffu, ratios, i * (kIterRows / 16) + crow / 16);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] = mul_f16x2(f[k], ratio);
+                }
+                const int row = i * kIterRows + crow;
+                *reinterpret_cast<uint4 *>(tile + dst_half + sw128_offset(row, chunk0)) = make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint4 *>(tile + dst_half + sw128_offset(row, chunk0 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+            }
+        };
+        // every thread's stores, then one arrival a warp
+        auto hand_over = [&](uint64_t *bar) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto stage_free = [&](uint64_t *bar, uint32_t parity) -> bool {
+            const bool free = mbar_wait(bar, parity, &abort_sh);
+            if (__any_sync(0xffffffffu, !free)) {
+                if (lane == 0) {
+                    abort_sh = 1;
+                    flag_error(a.dev_status, JSV_ERR_TIMEOUT);
+                }
+                return false;
+            }
+            return true;
+        };
+
+        float vref = 0.f, vratio = 0.f;
+        auto take_scale = [&](float vs) {                    // largest scale of a tile
+            vratio = 1.f;
+            if (vs > 2.f * vref) {
+                vratio = vref / vs;
+                vref = vs;
+            }
+        };
+        uint4 kw[kIters], vw[kIters];
+        int pages = load_pages(0), pages_next = load_pages(1);
+        float ks = 0.f, vs = 0.f;
+        auto load_scales = [&]() {
+            ks = vs = 0.f;
+            if (pages >= 0) {
+                const size_t block = (size_t)pages * a.Hkv + g;
+                ks = __ldg(p.c.k_scale + block);
+                vs = __ldg(p.c.v_scale + block);
+            }
+        };
+        load_codes(p.c.k, pages, kw);
+        load_scales();
+        load_codes(p.c.v, pages, vw);
+        bool ok = true;
+        for (int j = 0; j < n_pre; ++j) {
+            const int st = j % kStages;
+            const uint32_t ph = (uint32_t)((j / kStages) & 1);
+            uint8_t *sK = sKV + st * L::kStage, *sV = sK + L::kKV;
+            // the tile's scales: the largest V scale decides the reference
+            float top = fabsf(vs);
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            take_scale(__shfl_sync(0xffffffffu, top, 0));
+            if (warp == 0) {
+                if (lane < kTilePages)                       // a page past the prefix: its columns are masked
+                    info[j % kSlots].ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
+                if (lane == 0) {
+                    info[j % kSlots].vref = vref;
+                    info[j % kSlots].vratio = vratio;
+                }
+            }
+            const float ratio = vref > 0.f ? vs / vref : 0.f;
+            const uint32_t ratios = pack_f16(ratio, ratio);
+            ok = stage_free(&k_empty[st], ph ^ 1);
+            if (!ok) break;
+            store_codes(sK, kw, false, 0);
+            hand_over(&k_full[st]);
+            pages = pages_next;
+            load_codes(p.c.k, pages, kw);
+            load_scales();
+            ok = stage_free(&v_empty[st], ph ^ 1);
+            if (!ok) break;
+            store_codes(sV, vw, true, ratios);
+            hand_over(&v_full[st]);
+            load_codes(p.c.v, pages, vw);
+            pages_next = load_pages(j + 2);
+        }
+        // bf16 tiles: V first, so that what it says about its rows is there
+        // when the scores are
+        constexpr int kRow16 = D / 8;                        // 16-byte chunks of a bf16 row
+        constexpr int kIters16 = kTileKeys * kRow16 / kConvThreads;
+        constexpr int kBatch = 8;
+        const int trow = threadIdx.x / kRow16, tc = threadIdx.x % kRow16;
+        for (int j = n_pre; ok && j < ntiles; ++j) {
+            const int st = j % kStages;
+            const uint32_t ph = (uint32_t)((j / kStages) & 1);
+            const int slot0 = tail_slot(j);
+            TileInfo &ti = info[j % kSlots];
+            take_scale(1.f);
+            if (lane < kTileKeys / 32) ti.bad[warp][lane] = 0;
+            if (threadIdx.x == 0) {
+                ti.vref = vref;
+                ti.vratio = vratio;
+            }
+            __syncwarp();
+            for (int which = 1; ok && which >= 0; --which) {
+                const uint16_t *cache = which ? p.v : p.k;
+                uint8_t *tile = sKV + st * L::kStage + which * L::kKV;
+                ok = stage_free(which ? &v_empty[st] : &k_empty[st], ph ^ 1);
+                if (!ok) break;
+#pragma unroll
+                for (int i0 = 0; i0 < kIters16; i0 += kBatch) {
+                    uint4 w[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int row = (i0 + i) * (kConvThreads / kRow16) + trow, slot = slot0 + row;
+                        w[i] = make_uint4(0, 0, 0, 0);
+                        if (slot < r.P + r.n) {
+                            const long long pi = (long long)b * a.max_pages_per_req + slot / 16;
+                            const int page = JSV_IN_BOUNDS(pi, (long long)a.B * a.max_pages_per_req, a.dev_status)
+                                                 ? __ldg(a.page_table + pi) : -1;
+                            const size_t at = (((size_t)page * 16 + slot % 16) * a.Hkv + g) * D + tc * 8;
+                            if (page < 0 || page >= a.num_pages)
+                                flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                            else if (JSV_IN_BOUNDS(at + 7, (long long)a.num_pages * 16 * a.Hkv * D, a.dev_status))
+                                w[i] = *reinterpret_cast<const uint4 *>(cache + at);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int row = (i0 + i) * (kConvThreads / kRow16) + trow;
+                        if (which) {
+                            // a weight of zero does not undo an infinity or NaN in the
+                            // product: such a row is zeroed here and noted
+                            const uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                                        __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                            const unsigned odd = __ballot_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
+                            const unsigned mine = (kRow16 == 16 ? 0xffffu : 0xffu) << (lane / kRow16 * kRow16);
+                            if (odd & mine) {
+                                w[i] = make_uint4(0, 0, 0, 0);
+                                if (tc == 0) atomicOr(&ti.bad[warp][row >> 5], 1u << (row & 31));
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(tile + (tc >> 3) * (kTileKeys * 128) + sw128_offset(row, tc & 7)) = w[i];
+                    }
+                }
+                hand_over(which ? &v_full[st] : &k_full[st]);
+            }
+        }
+    } else if (warp < kSoftmaxWarp0) {
+        setmaxnreg_dec<kRegsMma>();
+        if (warp == kMmaWarp && lane == 0 && ntiles > 0) {
+            const uint32_t aQ = smem_addr(sQ), aKV = smem_addr(sKV);
+            if (ngroups > 1)
+                kv8_mma_loop<D, 2>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full, o_done,
+                                   &q_ready, &drain_bar, &abort_sh, a.dev_status);
+            else
+                kv8_mma_loop<D, 1>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full, o_done,
+                                   &q_ready, &drain_bar, &abort_sh, a.dev_status);
+        }
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        // ---------------------------------------------------------- softmax
+        const int grp = (warp - kSoftmaxWarp0) >> 2, sub = warp & 3;
+        const int grow = sub * 32 + lane, row = grp * kGroupRows + grow;
+        const uint32_t lane_addr = (uint32_t)(sub * 32) << 16;
+        const uint32_t tS = tmem + grp * 128 + lane_addr, tO = tmem + 256 + grp * D + lane_addr;
+        const int gt = threadIdx.x - 32 * (kSoftmaxWarp0 + 4 * grp);       // 0..127 in the group
+        const bool row_valid = row < rows_here;
+        const int rg = m0 + row, node = rg / G, head = g * G + rg % G;
+
+        // The group's rows of Q into its operand region, bf16 or, scaled by a
+        // power of two that brings the row's largest magnitude to [2^13, 2^14),
+        // fp16.  D / 8 neighbouring threads share a row.
+        constexpr int kRow16 = D / 8;
+        auto put_q = [&](bool as_f16) {
+            constexpr int kQIters = kGroupRows * kRow16 / 128;
+            constexpr int kQBatch = 8;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kQIters; i0 += kQBatch) {
+                uint4 w[kQBatch];
+#pragma unroll
+                for (int i = 0; i < kQBatch; ++i) {
+                    const int rr = (i0 + i) * (128 / kRow16) + gt / kRow16, c = gt % kRow16;
+                    const int rgg = m0 + grp * kGroupRows + rr;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (rgg < rows_total) {
+                        const size_t qi = ((size_t)(r.base + rgg / G) * a.Hq + g * G + rgg % G) * D + c * 8;
+                        if (JSV_IN_BOUNDS(qi + 7, (long long)a.total_nodes * a.Hq * D, a.dev_status))
+                            w[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + qi));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kQBatch; ++i) {
+                    const int rr = (i0 + i) * (128 / kRow16) + gt / kRow16, c = gt % kRow16;
+                    if (as_f16) {
+                        uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                              __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                        m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+                        for (int off = 1; off < kRow16; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+                        const int ex = min(max((int)(m >> 7), 14), 254);
+                        const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
+                        if (c == 0)      // kept normal, so that a masked score stays -inf under it
+                            row_fac[grp * kGroupRows + rr] =
+                                fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23), 1.2e-38f);
+                        auto two = [&](uint32_t x) {
+                            return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+                        };
+                        w[i] = make_uint4(two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
+                    }
+                    *reinterpret_cast<uint4 *>(sQ + grp * L::kQGroup + (c >> 3) * (kGroupRows * 128) +
+                                               sw128_offset(rr, c & 7)) = w[i];
+                }
+            }
+            fence_async_smem();
+        };
+        put_q(n_pre > 0);
+        if (has_tail)
+            for (int i = threadIdx.x - 32 * kSoftmaxWarp0; i < r.n; i += kGroups * 128)
+                par_sh[i] = JSV_IN_BOUNDS(r.base + i, a.total_nodes, a.dev_status) ? __ldg(a.parent + r.base + i) : -1;
+        named_barrier(1, kGroups * 128);         // Q, row factors and parents are in place
+        if (lane == 0) mbar_arrive(&q_ready);
+        const float fac = row_fac[row];
+        if (has_tail && row_valid) {
+            for (int w = 0; w < kTreeWords; ++w) anc[row][w] = 0;
+            int j = node;
+            while (j != -1) {
+                anc[row][j >> 5] |= 1u << (j & 31);
+                const int pj = par_sh[j];
+                if (j == 0 ? pj != -1 : (pj < 0 || pj >= j)) {
+                    flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                    break;
+                }
+                j = pj;
+            }
+        }
+
+        float m_used = -INFINITY, l = 0.f, vref = 0.f;
+        bool ok = true;
+        const int my_tiles = grp < ngroups ? ntiles : 0;
+        auto one_tile = [&](int j, auto tail_c) -> bool {
+            constexpr bool is_tail = decltype(tail_c)::value;
+            if (!mbar_wait(&s_full[grp], j & 1, &abort_sh)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                return false;
+            }
+            tc_fence_after();
+            const TileInfo &ti = info[j % kSlots];
+            uint32_t sv[kTileKeys / 32][32];
+#pragma unroll
+            for (int c = 0; c < kTileKeys / 32; ++c) tmem_ld_32x32b_x32(tS + c * 32, sv[c]);
+            // what brings each page's 16 columns to log2 units
+            float cs[kTilePages];
+            if constexpr (!is_tail) {
+                const float4 k0 = *reinterpret_cast<const float4 *>(&ti.ks[0]);
+                const float4 k1 = *reinterpret_cast<const float4 *>(&ti.ks[4]);
+                cs[0] = fac * k0.x, cs[1] = fac * k0.y, cs[2] = fac * k0.z, cs[3] = fac * k0.w;
+                cs[4] = fac * k1.x, cs[5] = fac * k1.y, cs[6] = fac * k1.z, cs[7] = fac * k1.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTilePages; ++k) cs[k] = p.scale_log2;
+            }
+            const float vratio = ti.vratio;
+            vref = ti.vref;
+            tmem_ld_wait();
+            if constexpr (is_tail) {
+                const int slot0 = tail_slot(j);
+#pragma unroll
+                for (int c = 0; c < kTileKeys / 32; ++c) {
+                    const int j0 = slot0 + c * 32 - r.P;         // tree node of column 32c (< 0: prefix, seen by all)
+                    uint32_t vis = 0u;
+                    if (row_valid) {
+                        if (j0 <= -32) {
+                            vis = 0xffffffffu;
+                        } else if (j0 < 0) {
+                            vis = (anc[row][0] << (-j0)) | ((1u << (-j0)) - 1u);
+                        } else if (j0 < kMaxTreeNodes) {
+                            const int w = j0 >> 5;
+                            vis = __funnelshift_r(anc[row][w], w + 1 < kTreeWords ? anc[row][w + 1] : 0u, j0 & 31);
+                        }
+                        if (vis & (ti.bad[0][c] | ti.bad[1][c] | ti.bad[2][c] | ti.bad[3][c])) l = __uint_as_float(0x7fc00000u);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) sv[c][x] = ((vis >> x) & 1u) ? sv[c][x] : 0xff800000u;
+                }
+            } else if ((t_begin + j + 1) * kTilePages > pages8) {
+                const int nb = pages8 - (t_begin + j) * kTilePages;         // pages this tile holds
+#pragma unroll
+                for (int c = 0; c < kTileKeys / 32; ++c)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (2 * c + x / 16 >= nb) sv[c][x] = 0xff800000u;
+            }
+            // row maximum, a page at a time (scales are not negative)
+            float tmax = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kTilePages; ++k) {
+                const uint32_t *s = &sv[k / 2][(k & 1) * 16];
+                float m0_ = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+                float m1_ = fmax3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+#pragma unroll
+                for (int x = 6; x < 14; x += 4) {
+                    m0_ = fmax3(m0_, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                    m1_ = fmax3(m1_, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+                }
+                m0_ = fmax3(m0_, __uint_as_float(s[14]), __uint_as_float(s[15]));
+                tmax = fmaxf(tmax, fmaxf(m0_, m1_) * cs[k]);
+            }
+            float m_new = m_used;
+            if (tmax > m_used + kMaxSlack) m_new = tmax;
+            const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);     // 0 when m_used = -inf
+            const float corr_o = corr * vratio;
+            // O holds the earlier tiles' sum under the old maximum and reference
+            // scale.  S_j was issued after PV_{j-1} and completes after it.
+            if (__any_sync(0xffffffffu, corr_o != 1.f) && j >= 1) {
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                    uint32_t ov[16];
+                    tmem_ld_32x32b_x16(tO + c0, ov);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * corr_o);
+                    tmem_st_32x32b_x16(tO + c0, ov);
+                }
+                tmem_st_wait();
+            }
+            const float base = m_new == -INFINITY ? kWeightLog2 : kWeightLog2 - m_new;
+            const uint64_t base2 = f2_pack(base, base);
+            uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+            // bf16 values carry no scale of their own: their weights take 1 / vref
+            const float unscale = is_tail ? 1.f / vref : 1.f;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int col = h * 32 + 2 * i;
+                    const float c = cs[col / 16];
+                    const uint64_t xa = f2_fma(f2_pack(__uint_as_float(sv[col / 32][col % 32]),
+                                                       __uint_as_float(sv[col / 32][col % 32 + 1])), f2_pack(c, c), base2);
+                    float u0, u1;
+                    f2_unpack(xa, u0, u1);
+                    u0 = fast_exp2(u0);
+                    u1 = fast_exp2(u1);
+                    ps2[i & 1] = f2_add(ps2[i & 1], f2_pack(u0, u1));
+                    pk[i] = is_tail ? pack_bf16x2(u0 * unscale, u1 * unscale) : pack_f16(u0, u1);
+                }
+                tmem_st_32x32b_x16(tS + h * 16, pk);
+            }
+            float q0, q1, q2, q3;
+            f2_unpack(ps2[0], q0, q1);
+            f2_unpack(ps2[1], q2, q3);
+            l = l * corr + ((q0 + q1) + (q2 + q3));
+            m_used = m_new;
+            tmem_st_wait();
+            // the next tile is bf16: so is Q from here on.  This group's S of the
+            // last 8-bit tile is complete, and the next is issued after these
+            // warps' arrivals.
+            if (!is_tail && has_tail && j + 1 == n_pre) put_q(false);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[grp]);
+            return true;
+        };
+        for (int j = 0; j < min(n_pre, my_tiles); ++j)
+            if (!one_tile(j, std::false_type{})) break;
+        for (int j = n_pre; ok && j < my_tiles; ++j)
+            if (!one_tile(j, std::true_type{})) break;
+
+        bool have_o = ok && my_tiles > 0;
+        if (have_o) {
+            if (!mbar_wait(&o_done[grp], (uint32_t)((my_tiles - 1) & 1), &abort_sh)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) have_o = false;
+        }
+        if (!have_o) {
+            m_used = -INFINITY;
+            l = 0.f;
+            if (!ok) {
+                abort_sh = 1;
+                flag_error(a.dev_status, JSV_ERR_TIMEOUT);
+            }
+        }
+        // The rows, in whole rows through this warp's slice of the group's Q
+        // region (every product of the group has completed), half of D at a time.
+        const size_t rows = (size_t)a.total_nodes * a.Hq;
+        const size_t row_id = (size_t)(r.base + min(node, r.n - 1)) * a.Hq + head;
+        constexpr int kScrCols = D / 2, kChunks = kScrCols / 4, kRowsPerStore = 32 / kChunks;
+        float4 *scr = reinterpret_cast<float4 *>(sQ + grp * L::kQGroup + sub * (32 * kScrCols * 4));
+        if (have_o) tc_fence_after();
+        auto write_rows = [&](long long my_off, float scale, auto store) {
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+                for (int c0 = 0; c0 < kScrCols; c0 += 32) {
+                    uint32_t rr[32];
+                    if (have_o) {
+                        tmem_ld_32x32b_x32(tO + pass * kScrCols + c0, rr);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) rr[x] = 0u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        scr[lane * kChunks + ((c0 / 4 + x) ^ (lane & (kChunks - 1)))] =
+                            make_float4(__uint_as_float(rr[4 * x]) * scale, __uint_as_float(rr[4 * x + 1]) * scale,
+                                        __uint_as_float(rr[4 * x + 2]) * scale, __uint_as_float(rr[4 * x + 3]) * scale);
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kRowsPerStore) {
+                    const int wr = i + lane / kChunks, ch = lane % kChunks;
+                    const long long off = __shfl_sync(0xffffffffu, my_off, wr);
+                    const float4 v = scr[wr * kChunks + (ch ^ (wr & (kChunks - 1)))];
+                    if (off >= 0) store(off + pass * kScrCols + ch * 4, v);
+                }
+                __syncwarp();
+            }
+        };
+        if (Sb == 1) {
+            write_rows(row_valid ? (long long)(row_id * D) : -1ll, l == 0.f ? 0.f : vref / l,
+                       [&](long long o, const float4 &v) {
+                           if (JSV_IN_BOUNDS(o + 3, (long long)rows * D, a.dev_status))
+                               *reinterpret_cast<uint2 *>(p.out + o) = make_uint2(pack_bf16x2(v.x, v.y),
+                                                                                  pack_bf16x2(v.z, v.w));
+                       });
+        } else {
+            write_rows(row_valid ? (long long)(((size_t)split * rows + row_id) * D) : -1ll, vref,
+                       [&](long long o, const float4 &v) {
+                           if (JSV_IN_BOUNDS(o + 3, (long long)p.S * rows * D, a.dev_status))
+                               *reinterpret_cast<float4 *>(p.ws_o + o) = v;
+                       });
+            const size_t mi = (size_t)split * rows + row_id;
+            if (row_valid && JSV_IN_BOUNDS(mi, (long long)p.S * rows, a.dev_status))
+                *reinterpret_cast<float2 *>(p.ws_ml + mi * 2) = make_float2(m_used, l);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int FMT>
+static cudaError_t launch_tiles(const Kv8Params &p, cudaStream_t st) {
+    using L = TileSmem<D>;
+    auto kernel = kv8_tiles_kernel<D, FMT>;
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([&]() {
+        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     (int)cudaSharedmemCarveoutMaxShared);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    const int G = p.a.Hq / p.a.Hkv;
+    dim3 grid((p.a.max_nodes * G + kRowsPerCta - 1) / kRowsPerCta, p.S, p.a.B * p.a.Hkv);
+    e = launch_pdl(kernel, grid, dim3(kTileThreads), L::kTotal, st, p);
+    if (e != cudaSuccess) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kernel) == cudaSuccess)
+            note_launch_failure("tree attention over 8-bit pages", fa.numRegs, fa.maxThreadsPerBlock, fa.sharedSizeBytes,
+                                fa.maxDynamicSharedSizeBytes, kTileThreads, L::kTotal);
+        return e;
+    }
+    count_launches(1);
+    return cudaSuccess;
+}
+
+cudaError_t launch_kv8_tiles(const Kv8Params &p, cudaStream_t st) {
+    const bool e4m3 = p.c.format == JSV_KV8_E4M3;
+    if (p.a.D == 128) return e4m3 ? launch_tiles<128, JSV_KV8_E4M3>(p, st) : launch_tiles<128, JSV_KV8_INT8>(p, st);
+    return e4m3 ? launch_tiles<64, JSV_KV8_E4M3>(p, st) : launch_tiles<64, JSV_KV8_INT8>(p, st);
+}
+
+}  // namespace jsv
