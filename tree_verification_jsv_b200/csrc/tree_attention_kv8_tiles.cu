@@ -6,7 +6,7 @@
 // two 128-row groups that take turns on the tensor core, as in
 // tree_attention.cu, whose MMA order and softmax this kernel keeps.  What
 // differs is where the operands come from: the codes are read by ordinary
-// 16-byte loads and written to the operand tiles as fp16 by four converting
+// 16-byte loads and written to the operand tiles as fp16 by seven converting
 // warps, one 128-key tile ahead, so the tensor core, the softmax and the
 // conversion run side by side.
 //
@@ -15,8 +15,9 @@
 // multiplied as bf16: a group's warps put their rows of Q back as bf16 when
 // they hand over the last 8-bit tile's weights.
 //
-//   warps 0..3    codes -> fp16 tiles, scales; bf16 tiles
-//   warp 4        TMEM, MMA issue (one thread); 5..7 idle
+//   warps 0..3    V tiles: codes -> fp16, or bf16 copied
+//   warp 4        TMEM, MMA issue (one thread)
+//   warps 5..7    K tiles likewise, and the tiles' scales
 //   warps 8..15   softmax, one query row per thread
 //
 // The K scale of a page multiplies its 16 score columns (it rides on the
@@ -42,15 +43,16 @@ constexpr int kRowsPerCta = kGroups * kGroupRows;
 constexpr int kTileKeys = 128;
 constexpr int kTilePages = kTileKeys / 16;
 constexpr int kStages = 2;
-constexpr int kConvThreads = 128;
+constexpr int kVTeam = 4;                        // converting warps of V (0..3) and of K (5..7)
+constexpr int kKTeam = 3;
 constexpr int kMmaWarp = 4;
 constexpr int kSoftmaxWarp0 = 8;
 constexpr int kTileThreads = 512;
-// registers a thread after the split, of 128 at launch: 112 + 48 + 2 * 176 =
+// registers a thread after the split, of 128 at launch: 48 + 48 + 2 * 208 =
 // 4 * 128 over the four warpgroups
-constexpr int kRegsConv = 112;
+constexpr int kRegsConv = 48;
 constexpr int kRegsMma = 48;
-constexpr int kRegsSoftmax = 176;
+constexpr int kRegsSoftmax = 208;
 constexpr int kSlots = 4;                        // tiles whose scales are held, see TileInfo
 constexpr float kWeightLog2 = 6.f;               // weights are held as 2^6 e: e <= 2^8 stays inside fp16
 
@@ -61,7 +63,7 @@ struct __align__(16) TileInfo {
     float ks[kTilePages];                        // read as two float4
     float vref, vratio;                          // reference scale, and the previous one over it
     // bf16 slots whose V row is not finite, as each converting warp found them
-    uint32_t bad[kConvThreads / 32][kTileKeys / 32];
+    uint32_t bad[kVTeam][kTileKeys / 32];
 };
 
 template <int D>
@@ -70,7 +72,8 @@ struct TileSmem {
     static constexpr int kQ = kGroups * kQGroup;
     static constexpr int kKV = kTileKeys * D * 2;              // one K (or V) tile
     static constexpr int kStage = 2 * kKV;
-    static constexpr int kTotal = kQ + kStages * kStage + 1024;
+    static constexpr int kRaw = kTileKeys * D;                 // one tile's codes of K (or V)
+    static constexpr int kTotal = kQ + kStages * kStage + 2 * kRaw + 1024;
 };
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -95,8 +98,12 @@ __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_
     uint64_t dQ = desc_kmajor_sw128(aQ);
     uint64_t dK0 = desc_kmajor_sw128(aKV);
     uint64_t dV0 = desc_mnmajor_sw128(aKV + L::kKV, kTileKeys * 128, 1024);
-    auto issue_s = [&](auto grp_c, uint64_t dk, uint32_t type) {
+    // the operand type is a constant of each call: a descriptor formed at run
+    // time between two MMAs sits on the tensor pipe's critical path (with it the
+    // 16 MMAs of a group took 3,400 cycles to issue instead of about 1,100)
+    auto issue_s_typed = [&](auto grp_c, auto type_c, uint64_t dk) {
         constexpr int grp = decltype(grp_c)::value;
+        constexpr uint32_t type = decltype(type_c)::value;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = grp * L::kQGroup + (kk >> 2) * (kGroupRows * 128) + (kk & 3) * 32;
@@ -105,13 +112,24 @@ __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_
         }
         mma_commit(&s_full[grp]);
     };
-    auto issue_pv = [&](auto grp_c, uint64_t dv, uint32_t acc_first, uint32_t type) {
+    auto issue_pv_typed = [&](auto grp_c, auto type_c, uint64_t dv, uint32_t acc_first) {
         constexpr int grp = decltype(grp_c)::value;
+        constexpr uint32_t type = decltype(type_c)::value;
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
             mma_bf16_ts(tmem + 256 + grp * D, tmem + grp * 128 + kk * 8, dv + ((kk * 2048) >> 4), id_o | type,
                         kk > 0 ? 1u : acc_first);
         mma_commit(&o_done[grp]);
+    };
+    using F16 = std::integral_constant<uint32_t, 0u>;
+    using BF16 = std::integral_constant<uint32_t, kBf16>;
+    auto issue_s = [&](auto grp_c, bool codes, uint64_t dk) {
+        if (codes) issue_s_typed(grp_c, F16{}, dk);
+        else issue_s_typed(grp_c, BF16{}, dk);
+    };
+    auto issue_pv = [&](auto grp_c, bool codes, uint64_t dv, uint32_t acc_first) {
+        if (codes) issue_pv_typed(grp_c, F16{}, dv, acc_first);
+        else issue_pv_typed(grp_c, BF16{}, dv, acc_first);
     };
     using G0 = std::integral_constant<int, 0>;
     using G1 = std::integral_constant<int, 1>;
@@ -119,9 +137,8 @@ __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_
     if (ok) ok = mbar_wait(&k_full[0], 0, abort_sh);
     if (ok) {
         tc_fence_after();
-        const uint32_t type = n_pre > 0 ? 0u : kBf16;
-        issue_s(G0{}, dK0, type);
-        if constexpr (NG > 1) issue_s(G1{}, dK0, type);
+        issue_s(G0{}, n_pre > 0, dK0);
+        if constexpr (NG > 1) issue_s(G1{}, n_pre > 0, dK0);
         mma_commit(&k_empty[0]);
     }
     for (int j = 0; ok && j < ntiles; ++j) {
@@ -131,26 +148,26 @@ __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_
         const bool more = j + 1 < ntiles;
         const uint64_t dv = dV0 + st * kStageStep, dkn = dK0 + stn * kStageStep;
         const uint32_t acc_first = j > 0 ? 1u : 0u;
-        const uint32_t type = j < n_pre ? 0u : kBf16, type_n = j + 1 < n_pre ? 0u : kBf16;
+        const bool codes = j < n_pre, codes_n = j + 1 < n_pre;
         ok = mbar_wait(&v_full[st], ph, abort_sh) && (!more || mbar_wait(&k_full[stn], phn, abort_sh));
         if (!ok) break;
         ok = mbar_wait(&p_full[0], j & 1, abort_sh);
         if (!ok) break;
         tc_fence_after();
-        issue_pv(G0{}, dv, acc_first, type);
+        issue_pv(G0{}, codes, dv, acc_first);
         if constexpr (NG == 1) mma_commit(&v_empty[st]);
         if (more) {
-            issue_s(G0{}, dkn, type_n);
+            issue_s(G0{}, codes_n, dkn);
             if constexpr (NG == 1) mma_commit(&k_empty[stn]);
         }
         if constexpr (NG > 1) {
             ok = mbar_wait(&p_full[1], j & 1, abort_sh);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(G1{}, dv, acc_first, type);
+            issue_pv(G1{}, codes, dv, acc_first);
             mma_commit(&v_empty[st]);
             if (more) {
-                issue_s(G1{}, dkn, type_n);
+                issue_s(G1{}, codes_n, dkn);
                 mma_commit(&k_empty[stn]);
             }
         }
@@ -174,13 +191,11 @@ kv8_tiles_kernel(const Kv8Params p) {
     using L = TileSmem<D>;
     extern __shared__ uint8_t dsmem[];
     __shared__ __align__(8) uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
-    __shared__ __align__(8) uint64_t s_full[kGroups], p_full[kGroups], o_done[kGroups], q_ready, drain_bar;
+    __shared__ __align__(8) uint64_t s_full[kGroups], p_full[kGroups], o_done[kGroups], q_ready, tree_read, drain_bar, raw_full[kVTeam + kKTeam];
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_sh;
     __shared__ TileInfo info[kSlots];
-    __shared__ float row_fac[kRowsPerCta];
-    __shared__ uint32_t anc[kRowsPerCta][kTreeWords];
-    __shared__ int par_sh[kMaxTreeNodes];
+    __shared__ float row_inv[kRowsPerCta];        // what undoes the scaling of each row of Q
 
     const BatchArgs &a = p.a;
     const int G = a.Hq / a.Hkv;
@@ -205,13 +220,15 @@ kv8_tiles_kernel(const Kv8Params p) {
     auto tail_slot = [&](int j) { return P0 + (t_begin + j - pre_tiles) * kTileKeys; };
 
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sKV = smem + L::kQ;
+    uint8_t *sQ = smem, *sKV = smem + L::kQ, *raw = sKV + kStages * L::kStage;
+    // the request's parents, over the second V tile until the ancestors are found
+    int *par_sh = reinterpret_cast<int *>(sKV + L::kStage + L::kKV);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&k_full[s], kConvThreads / 32);
-            mbar_init(&v_full[s], kConvThreads / 32);
+            mbar_init(&k_full[s], kKTeam);
+            mbar_init(&v_full[s], kVTeam);
             mbar_init(&k_empty[s], 1);
             mbar_init(&v_empty[s], 1);
         }
@@ -221,7 +238,9 @@ kv8_tiles_kernel(const Kv8Params p) {
             mbar_init(&o_done[s], 1);
         }
         mbar_init(&q_ready, 4 * kGroups);
+        mbar_init(&tree_read, 4 * kGroups);
         mbar_init(&drain_bar, 1);
+        for (int w = 0; w < kVTeam + kKTeam; ++w) mbar_init(&raw_full[w], 1);
         abort_sh = 0;
         fence_barrier_init();
     }
@@ -234,23 +253,32 @@ kv8_tiles_kernel(const Kv8Params p) {
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
 
-    if (warp < kConvThreads / 32) {
-        setmaxnreg_dec<kRegsConv>();
-        // ------------------------------------------------------- conversion
-        // A tile's codes are eight contiguous blocks of 16 * D bytes.  A warp's
-        // lanes take 16-byte chunks so that eight neighbouring lanes store to
-        // two rows with an even and an odd number: their swizzled 16-byte
-        // columns then cover all 32 banks.
-        constexpr int kRowChunks = D / 16;                   // 16-byte chunks of codes in a row
-        constexpr int kIters = kTileKeys * kRowChunks / kConvThreads;
-        constexpr int kIterRows = kTileKeys / kIters;        // rows of one iteration: 16 or 32
-        const int crow = D == 128 ? warp * 4 + ((lane >> 4) << 1) + ((lane >> 2) & 1) : warp * 8 + (lane >> 2);
-        const int cc = D == 128 ? (lane & 3) | (((lane >> 3) & 1) << 2) : lane & 3;
-        const uint32_t code_off = (crow % 16) * D + cc * 16;
-        // byte offset of this thread's 32 bytes of row crow, first half
-        const uint32_t dst_half = (cc >> 2) * (kTileKeys * 128);
-        const int chunk0 = (cc & 3) * 2;
-        const long long code_bytes = (long long)p.c.num_pages * a.Hkv * 16 * D;
+    // ----------------------------------------------------------- conversion
+    // One team of warps fills the K tiles, another the V tiles.  `me` is the
+    // warp's number in a team of kTeam.
+    auto convert = [&](auto is_v_c, auto team_c, int me) {
+        constexpr bool is_v = decltype(is_v_c)::value;
+        constexpr int kTeam = decltype(team_c)::value;
+        // A warp takes the pages me, me + kTeam, ... of each tile.  Their codes
+        // come as one bulk copy each into the warp's own part of `raw`, one tile
+        // ahead: no warp waits for another, and the loop over pages is short and
+        // rolled, so that it and the softmax's code fit the instruction caches
+        // together.  (Codes copied by every lane, or held in registers, which
+        // the softmax then lacks: 6-20% slower.)
+        // The page is read and stored in units of 512 bytes, 16 bytes a lane (4
+        // rows at D = 128, 8 at D = 64).  Of eight neighbouring lanes four take
+        // half a row of 128 bytes and four the other half of the next row: they
+        // read all 32 banks, and the two rows' swizzled columns store to all.
+        constexpr int kBlock = 16 * D;                       // codes of a page and head
+        constexpr int kUnits = kBlock / 512;
+        constexpr int kUnitRows = 16 / kUnits;
+        const int urow = D == 128 ? ((lane >> 4) << 1) + ((lane >> 2) & 1) : lane >> 2;
+        const int cc = D == 128 ? (lane & 3) | ((((lane >> 2) ^ (lane >> 3)) & 1) << 2) : lane & 3;
+        const uint8_t *codes = is_v ? p.c.v : p.c.k;
+        uint8_t *my_raw = raw + (is_v ? L::kRaw : 0);
+        uint8_t *tiles = sKV + (is_v ? L::kKV : 0) + (cc >> 2) * (kTileKeys * 128);
+        uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+        uint64_t *landed = &raw_full[is_v ? me : kVTeam + me];
 
         // lane l < 8: page l of a tile (-1: reads zeros)
         auto load_pages = [&](int j) -> int {
@@ -260,37 +288,51 @@ kv8_tiles_kernel(const Kv8Params p) {
                 const long long pi = (long long)b * p.c.max_pages_per_req + lp;
                 if (JSV_IN_BOUNDS(pi, (long long)a.B * p.c.max_pages_per_req, a.dev_status)) page = __ldg(p.c.page_table + pi);
                 if (page < 0 || page >= p.c.num_pages) {
-                    if (warp == 0) flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                    flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
                     page = -1;
                 }
             }
             return page;
         };
-        auto load_codes = [&](const uint8_t *codes, int pages, uint4 (&w)[kIters]) {
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                const int page = __shfl_sync(0xffffffffu, pages, i * (kIterRows / 16) + crow / 16);
-                const size_t at = ((size_t)page * a.Hkv + g) * 16 * D + code_off;
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (page >= 0 && JSV_IN_BOUNDS(at + 15, code_bytes, a.dev_status))
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + at));
-            }
+        auto fetch = [&](int pages) {                        // every lane is done with the last tile's
+            const bool mine = pages >= 0 && (lane + kTeam - me) % kTeam == 0;
+            const unsigned all = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) mbar_arrive_expect_tx(landed, __popc(all) * kBlock);
+            __syncwarp();
+            if (mine)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 smem_addr(my_raw + lane * kBlock)),
+                             "l"(codes + ((size_t)pages * a.Hkv + g) * kBlock), "r"(kBlock), "r"(smem_addr(landed))
+                             : "memory");
         };
-        auto store_codes = [&](uint8_t *tile, const uint4 (&w)[kIters], bool scaled, uint32_t ratios) {
+        auto store = [&](uint8_t *tile, int pages, uint32_t ratios) {
+            const int chunk = (cc & 3) * 2;
+#pragma unroll 1
+            for (int pg = me; pg < kTilePages; pg += kTeam) {
+                const bool there = __shfl_sync(0xffffffffu, pages, pg) >= 0;
+                const uint32_t ratio = is_v ? __shfl_sync(0xffffffffu, ratios, pg) : 0u;
+                uint4 w[kUnits];
 #pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t f[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) codes_to_f16<FMT>(in[k], f[2 * k], f[2 * k + 1]);
-                if (scaled) {
-                    const uint32_t ratio = __shfl_sync(0xffffffffu, ratios, i * (kIterRows / 16) + crow / 16);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = mul_f16x2(f[k], ratio);
+                for (int u = 0; u < kUnits; ++u) {
+                    w[u] = make_uint4(0, 0, 0, 0);
+                    if (there)
+                        w[u] = *reinterpret_cast<const uint4 *>(my_raw + pg * kBlock + u * 512 + urow * D + cc * 16);
                 }
-                const int row = i * kIterRows + crow;
-                *reinterpret_cast<uint4 *>(tile + dst_half + sw128_offset(row, chunk0)) = make_uint4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<uint4 *>(tile + dst_half + sw128_offset(row, chunk0 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) codes_to_f16<FMT>(in[k], f[2 * k], f[2 * k + 1]);
+                    if constexpr (is_v) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = mul_f16x2(f[k], ratio);
+                    }
+                    const int row = u * kUnitRows + urow;
+                    uint8_t *to = tile + pg * 2048;
+                    *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
             }
         };
         // every thread's stores, then one arrival a warp
@@ -299,9 +341,9 @@ kv8_tiles_kernel(const Kv8Params p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        auto stage_free = [&](uint64_t *bar, uint32_t parity) -> bool {
-            const bool free = mbar_wait(bar, parity, &abort_sh);
-            if (__any_sync(0xffffffffu, !free)) {
+        auto wait_for = [&](uint64_t *bar, uint32_t parity) -> bool {
+            const bool done = mbar_wait(bar, parity, &abort_sh);
+            if (__any_sync(0xffffffffu, !done)) {
                 if (lane == 0) {
                     abort_sh = 1;
                     flag_error(a.dev_status, JSV_ERR_TIMEOUT);
@@ -310,8 +352,12 @@ kv8_tiles_kernel(const Kv8Params p) {
             }
             return true;
         };
+        // the second V tile's place holds the request's parents at first
+        auto stage_free = [&](int j) -> bool {
+            return wait_for(&empty[j % kStages], ((j / kStages) & 1) ^ 1) && (!is_v || j != 1 || wait_for(&tree_read, 0));
+        };
 
-        float vref = 0.f, vratio = 0.f;
+        float vref = 0.f, vratio = 0.f;                      // both teams keep the same reference
         auto take_scale = [&](float vs) {                    // largest scale of a tile
             vratio = 1.f;
             if (vs > 2.f * vref) {
@@ -319,119 +365,131 @@ kv8_tiles_kernel(const Kv8Params p) {
                 vref = vs;
             }
         };
-        uint4 kw[kIters], vw[kIters];
         int pages = load_pages(0), pages_next = load_pages(1);
         float ks = 0.f, vs = 0.f;
         auto load_scales = [&]() {
             ks = vs = 0.f;
             if (pages >= 0) {
                 const size_t block = (size_t)pages * a.Hkv + g;
-                ks = __ldg(p.c.k_scale + block);
+                if constexpr (!is_v) ks = __ldg(p.c.k_scale + block);
                 vs = __ldg(p.c.v_scale + block);
             }
         };
-        load_codes(p.c.k, pages, kw);
+        fetch(pages);
         load_scales();
-        load_codes(p.c.v, pages, vw);
         bool ok = true;
         for (int j = 0; j < n_pre; ++j) {
-            const int st = j % kStages;
-            const uint32_t ph = (uint32_t)((j / kStages) & 1);
-            uint8_t *sK = sKV + st * L::kStage, *sV = sK + L::kKV;
             // the tile's scales: the largest V scale decides the reference
             float top = fabsf(vs);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             take_scale(__shfl_sync(0xffffffffu, top, 0));
-            if (warp == 0) {
+            if (!is_v && me == 0) {
+                TileInfo &ti = info[j % kSlots];
                 if (lane < kTilePages)                       // a page past the prefix: its columns are masked
-                    info[j % kSlots].ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
+                    ti.ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
                 if (lane == 0) {
-                    info[j % kSlots].vref = vref;
-                    info[j % kSlots].vratio = vratio;
+                    ti.vref = vref;
+                    ti.vratio = vratio;
                 }
             }
             const float ratio = vref > 0.f ? vs / vref : 0.f;
-            const uint32_t ratios = pack_f16(ratio, ratio);
-            ok = stage_free(&k_empty[st], ph ^ 1);
+            ok = wait_for(landed, j & 1) && stage_free(j);
             if (!ok) break;
-            store_codes(sK, kw, false, 0);
-            hand_over(&k_full[st]);
+            store(tiles + (j % kStages) * L::kStage, pages, pack_f16(ratio, ratio));
+            hand_over(&full[j % kStages]);
             pages = pages_next;
-            load_codes(p.c.k, pages, kw);
+            fetch(pages);
             load_scales();
-            ok = stage_free(&v_empty[st], ph ^ 1);
-            if (!ok) break;
-            store_codes(sV, vw, true, ratios);
-            hand_over(&v_full[st]);
-            load_codes(p.c.v, pages, vw);
             pages_next = load_pages(j + 2);
         }
-        // bf16 tiles: V first, so that what it says about its rows is there
-        // when the scores are
+        if (!ok) {                                           // copies in flight land before this warp leaves
+            int zero = 0;
+            mbar_wait(landed, 0, (volatile int *)&zero);
+            mbar_wait(landed, 1, (volatile int *)&zero);
+        }
+        // bf16 tiles, copied asynchronously to their places, all of a tile's rows
+        // at once.  K is handed over after V, so that what is noted about V's rows
+        // is there when the scores are.
         constexpr int kRow16 = D / 8;                        // 16-byte chunks of a bf16 row
-        constexpr int kIters16 = kTileKeys * kRow16 / kConvThreads;
-        constexpr int kBatch = 8;
-        const int trow = threadIdx.x / kRow16, tc = threadIdx.x % kRow16;
+        constexpr int kTailUnits = kTileKeys * kRow16 / 32;  // 512 bytes each
+        constexpr int kTailRows = 32 / kRow16;
+        const uint16_t *cache = is_v ? p.v : p.k;
+        const int trow = lane / kRow16, tc = lane % kRow16;
+        auto load_tail_pages = [&](int j) -> int {           // lane l < 8: page l of tile j
+            int page = -1;
+            const int lp = tail_slot(j) / 16 + lane;
+            if (lane < kTilePages && lp * 16 < r.P + r.n) {
+                const long long pi = (long long)b * a.max_pages_per_req + lp;
+                if (JSV_IN_BOUNDS(pi, (long long)a.B * a.max_pages_per_req, a.dev_status)) page = __ldg(a.page_table + pi);
+                if (page < 0 || page >= a.num_pages) {
+                    flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        int tail_pages = has_tail ? load_tail_pages(n_pre) : -1;
         for (int j = n_pre; ok && j < ntiles; ++j) {
-            const int st = j % kStages;
-            const uint32_t ph = (uint32_t)((j / kStages) & 1);
             const int slot0 = tail_slot(j);
             TileInfo &ti = info[j % kSlots];
             take_scale(1.f);
-            if (lane < kTileKeys / 32) ti.bad[warp][lane] = 0;
-            if (threadIdx.x == 0) {
+            if (is_v) {
+                if (lane < kTileKeys / 32) ti.bad[me][lane] = 0;
+                __syncwarp();
+            } else if (me == 0 && lane == 0) {
                 ti.vref = vref;
                 ti.vratio = vratio;
             }
-            __syncwarp();
-            for (int which = 1; ok && which >= 0; --which) {
-                const uint16_t *cache = which ? p.v : p.k;
-                uint8_t *tile = sKV + st * L::kStage + which * L::kKV;
-                ok = stage_free(which ? &v_empty[st] : &k_empty[st], ph ^ 1);
-                if (!ok) break;
-#pragma unroll
-                for (int i0 = 0; i0 < kIters16; i0 += kBatch) {
-                    uint4 w[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int row = (i0 + i) * (kConvThreads / kRow16) + trow, slot = slot0 + row;
-                        w[i] = make_uint4(0, 0, 0, 0);
-                        if (slot < r.P + r.n) {
-                            const long long pi = (long long)b * a.max_pages_per_req + slot / 16;
-                            const int page = JSV_IN_BOUNDS(pi, (long long)a.B * a.max_pages_per_req, a.dev_status)
-                                                 ? __ldg(a.page_table + pi) : -1;
-                            const size_t at = (((size_t)page * 16 + slot % 16) * a.Hkv + g) * D + tc * 8;
-                            if (page < 0 || page >= a.num_pages)
-                                flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
-                            else if (JSV_IN_BOUNDS(at + 7, (long long)a.num_pages * 16 * a.Hkv * D, a.dev_status))
-                                w[i] = *reinterpret_cast<const uint4 *>(cache + at);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int row = (i0 + i) * (kConvThreads / kRow16) + trow;
-                        if (which) {
-                            // a weight of zero does not undo an infinity or NaN in the
-                            // product: such a row is zeroed here and noted
-                            const uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                                        __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                            const unsigned odd = __ballot_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
-                            const unsigned mine = (kRow16 == 16 ? 0xffffu : 0xffu) << (lane / kRow16 * kRow16);
-                            if (odd & mine) {
-                                w[i] = make_uint4(0, 0, 0, 0);
-                                if (tc == 0) atomicOr(&ti.bad[warp][row >> 5], 1u << (row & 31));
-                            }
-                        }
-                        *reinterpret_cast<uint4 *>(tile + (tc >> 3) * (kTileKeys * 128) + sw128_offset(row, tc & 7)) = w[i];
+            ok = stage_free(j);
+            if (!ok) break;
+            uint8_t *tile = sKV + (is_v ? L::kKV : 0) + (j % kStages) * L::kStage + (tc >> 3) * (kTileKeys * 128);
+#pragma unroll 2
+            for (int u = me; u < kTailUnits; u += kTeam) {
+                const int row = u * kTailRows + trow;
+                const int page = __shfl_sync(0xffffffffu, tail_pages, u * kTailRows / 16);
+                const size_t at = (((size_t)max(page, 0) * 16 + row % 16) * a.Hkv + g) * D + tc * 8;
+                const bool in = page >= 0 && slot0 + row < r.P + r.n &&
+                                JSV_IN_BOUNDS(at + 7, (long long)a.num_pages * 16 * a.Hkv * D, a.dev_status);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(tile + sw128_offset(row, tc & 7))),
+                             "l"(cache + (in ? at : 0)), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+            if (j + 1 < ntiles) tail_pages = load_tail_pages(j + 1);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if constexpr (is_v) {
+                // a weight of zero does not undo an infinity or NaN in the
+                // product: such a row is zeroed here and noted
+#pragma unroll 4
+                for (int u = me; u < kTailUnits; u += kTeam) {
+                    const int row = u * kTailRows + trow;
+                    uint4 *at = reinterpret_cast<uint4 *>(tile + sw128_offset(row, tc & 7));
+                    const uint4 w = *at;
+                    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+                    const unsigned odd = __ballot_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
+                    const unsigned mine = (kRow16 == 16 ? 0xffffu : 0xffu) << (lane / kRow16 * kRow16);
+                    if (odd & mine) {
+                        *at = make_uint4(0, 0, 0, 0);
+                        if (tc == 0) atomicOr(&ti.bad[me][row >> 5], 1u << (row & 31));
                     }
                 }
-                hand_over(which ? &v_full[st] : &k_full[st]);
+            } else {
+                ok = wait_for(&v_full[j % kStages], (j / kStages) & 1);
+                if (!ok) break;
             }
+            hand_over(&full[j % kStages]);
         }
+    };
+
+    if (warp < kMmaWarp) {
+        setmaxnreg_dec<kRegsConv>();
+        convert(std::true_type{}, std::integral_constant<int, kVTeam>{}, warp);
     } else if (warp < kSoftmaxWarp0) {
         setmaxnreg_dec<kRegsMma>();
-        if (warp == kMmaWarp && lane == 0 && ntiles > 0) {
+        if (warp > kMmaWarp) {
+            convert(std::false_type{}, std::integral_constant<int, kKTeam>{}, warp - kMmaWarp - 1);
+        } else if (lane == 0 && ntiles > 0) {
             const uint32_t aQ = smem_addr(sQ), aKV = smem_addr(sKV);
             if (ngroups > 1)
                 kv8_mma_loop<D, 2>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full, o_done,
@@ -453,62 +511,78 @@ kv8_tiles_kernel(const Kv8Params p) {
 
         // The group's rows of Q into its operand region, bf16 or, scaled by a
         // power of two that brings the row's largest magnitude to [2^13, 2^14),
-        // fp16.  D / 8 neighbouring threads share a row.
+        // fp16.  D / 8 neighbouring threads share a row; all loads go out first.
         constexpr int kRow16 = D / 8;
-        auto put_q = [&](bool as_f16) {
-            constexpr int kQIters = kGroupRows * kRow16 / 128;
-            constexpr int kQBatch = 8;
-#pragma unroll 1
-            for (int i0 = 0; i0 < kQIters; i0 += kQBatch) {
-                uint4 w[kQBatch];
+        constexpr int kQIters = kGroupRows * kRow16 / 128;
+        const int qc = gt % kRow16;
+        uint8_t *q_at = sQ + grp * L::kQGroup + (qc >> 3) * (kGroupRows * 128);
+        {
+            const bool as_f16 = n_pre > 0;
+            const float inv_g = 1.f / (float)G;              // (row + 1/2) / G truncates to the node
+            uint4 w[kQIters];
 #pragma unroll
-                for (int i = 0; i < kQBatch; ++i) {
-                    const int rr = (i0 + i) * (128 / kRow16) + gt / kRow16, c = gt % kRow16;
-                    const int rgg = m0 + grp * kGroupRows + rr;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (rgg < rows_total) {
-                        const size_t qi = ((size_t)(r.base + rgg / G) * a.Hq + g * G + rgg % G) * D + c * 8;
-                        if (JSV_IN_BOUNDS(qi + 7, (long long)a.total_nodes * a.Hq * D, a.dev_status))
-                            w[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + qi));
-                    }
+            for (int i = 0; i < kQIters; ++i) {
+                const int rgg = m0 + grp * kGroupRows + i * (128 / kRow16) + gt / kRow16;
+                const int nd = (int)(((float)rgg + 0.5f) * inv_g);
+                const size_t qi = ((size_t)(r.base + nd) * a.Hq + g * G + (rgg - nd * G)) * D + qc * 8;
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (rgg < rows_total && JSV_IN_BOUNDS(qi + 7, (long long)a.total_nodes * a.Hq * D, a.dev_status))
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + qi));
+            }
+#pragma unroll
+            for (int i = 0; i < kQIters; ++i) {
+                const int rr = i * (128 / kRow16) + gt / kRow16;
+                if (as_f16) {
+                    uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                          __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                    m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+                    for (int off = 1; off < kRow16; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    const int ex = min(max((int)(m >> 7), 14), 254);
+                    const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
+                    if (qc == 0) row_inv[grp * kGroupRows + rr] = __uint_as_float((uint32_t)(ex - 13) << 23);
+                    auto two = [&](uint32_t x) {
+                        return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+                    };
+                    w[i] = make_uint4(two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
                 }
-#pragma unroll
-                for (int i = 0; i < kQBatch; ++i) {
-                    const int rr = (i0 + i) * (128 / kRow16) + gt / kRow16, c = gt % kRow16;
-                    if (as_f16) {
-                        uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                              __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                        m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-                        for (int off = 1; off < kRow16; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-                        const int ex = min(max((int)(m >> 7), 14), 254);
-                        const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
-                        if (c == 0)      // kept normal, so that a masked score stays -inf under it
-                            row_fac[grp * kGroupRows + rr] =
-                                fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23), 1.2e-38f);
-                        auto two = [&](uint32_t x) {
-                            return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-                        };
-                        w[i] = make_uint4(two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
-                    }
-                    *reinterpret_cast<uint4 *>(sQ + grp * L::kQGroup + (c >> 3) * (kGroupRows * 128) +
-                                               sw128_offset(rr, c & 7)) = w[i];
-                }
+                *reinterpret_cast<uint4 *>(q_at + sw128_offset(rr, qc & 7)) = w[i];
+            }
+            fence_async_smem();
+        }
+        // Back to bf16, in place.  Exact but for what lies 2^-28 and more below
+        // the row's largest, which fp16 rounded to a multiple of 2^-24.
+        auto q_to_bf16 = [&]() {
+#pragma unroll 4
+            for (int i = 0; i < kQIters; ++i) {
+                const int rr = i * (128 / kRow16) + gt / kRow16;
+                uint4 *at = reinterpret_cast<uint4 *>(q_at + sw128_offset(rr, qc & 7));
+                const uint4 w = *at;
+                const float inv = row_inv[grp * kGroupRows + rr];
+                auto two = [&](uint32_t x) {
+                    float lo, hi;
+                    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                        : "=f"(lo), "=f"(hi)
+                        : "r"(x));
+                    return pack_bf16x2(lo * inv, hi * inv);
+                };
+                *at = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
             }
             fence_async_smem();
         };
-        put_q(n_pre > 0);
         if (has_tail)
             for (int i = threadIdx.x - 32 * kSoftmaxWarp0; i < r.n; i += kGroups * 128)
                 par_sh[i] = JSV_IN_BOUNDS(r.base + i, a.total_nodes, a.dev_status) ? __ldg(a.parent + r.base + i) : -1;
         named_barrier(1, kGroups * 128);         // Q, row factors and parents are in place
         if (lane == 0) mbar_arrive(&q_ready);
-        const float fac = row_fac[row];
+        // kept normal, so that a masked score stays -inf under it
+        const float fac = fmaxf(p.scale_log2 * row_inv[row], 1.2e-38f);
+        uint32_t anc[kTreeWords];                // this row's ancestors and itself (local memory: read in bf16 tiles only)
         if (has_tail && row_valid) {
-            for (int w = 0; w < kTreeWords; ++w) anc[row][w] = 0;
+            for (int w = 0; w < kTreeWords; ++w) anc[w] = 0;
             int j = node;
             while (j != -1) {
-                anc[row][j >> 5] |= 1u << (j & 31);
+                anc[j >> 5] |= 1u << (j & 31);
                 const int pj = par_sh[j];
                 if (j == 0 ? pj != -1 : (pj < 0 || pj >= j)) {
                     flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
@@ -517,6 +591,9 @@ kv8_tiles_kernel(const Kv8Params p) {
                 j = pj;
             }
         }
+
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tree_read);
 
         float m_used = -INFINITY, l = 0.f, vref = 0.f;
         bool ok = true;
@@ -530,6 +607,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             }
             tc_fence_after();
             const TileInfo &ti = info[j % kSlots];
+            // the whole row of 128 scores in registers: one TMEM round trip
             uint32_t sv[kTileKeys / 32][32];
 #pragma unroll
             for (int c = 0; c < kTileKeys / 32; ++c) tmem_ld_32x32b_x32(tS + c * 32, sv[c]);
@@ -547,6 +625,8 @@ kv8_tiles_kernel(const Kv8Params p) {
             const float vratio = ti.vratio;
             vref = ti.vref;
             tmem_ld_wait();
+            // columns that are not seen become -inf: by a word of the tree's
+            // visibility for 32 columns, or whole pages past the prefix in its last tile
             if constexpr (is_tail) {
                 const int slot0 = tail_slot(j);
 #pragma unroll
@@ -557,38 +637,40 @@ kv8_tiles_kernel(const Kv8Params p) {
                         if (j0 <= -32) {
                             vis = 0xffffffffu;
                         } else if (j0 < 0) {
-                            vis = (anc[row][0] << (-j0)) | ((1u << (-j0)) - 1u);
+                            vis = (anc[0] << (-j0)) | ((1u << (-j0)) - 1u);
                         } else if (j0 < kMaxTreeNodes) {
                             const int w = j0 >> 5;
-                            vis = __funnelshift_r(anc[row][w], w + 1 < kTreeWords ? anc[row][w + 1] : 0u, j0 & 31);
+                            vis = __funnelshift_r(anc[w], w + 1 < kTreeWords ? anc[w + 1] : 0u, j0 & 31);
                         }
                         if (vis & (ti.bad[0][c] | ti.bad[1][c] | ti.bad[2][c] | ti.bad[3][c])) l = __uint_as_float(0x7fc00000u);
                     }
 #pragma unroll
                     for (int x = 0; x < 32; ++x) sv[c][x] = ((vis >> x) & 1u) ? sv[c][x] : 0xff800000u;
                 }
-            } else if ((t_begin + j + 1) * kTilePages > pages8) {
-                const int nb = pages8 - (t_begin + j) * kTilePages;         // pages this tile holds
+            } else {
+                const int nb = pages8 - (t_begin + j) * kTilePages;        // pages this tile holds
+                if (nb < kTilePages) {
 #pragma unroll
-                for (int c = 0; c < kTileKeys / 32; ++c)
+                    for (int c = 0; c < kTileKeys / 32; ++c)
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (2 * c + x / 16 >= nb) sv[c][x] = 0xff800000u;
+                        for (int x = 0; x < 32; ++x)
+                            if (2 * c + x / 16 >= nb) sv[c][x] = 0xff800000u;
+                }
             }
             // row maximum, a page at a time (scales are not negative)
             float tmax = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kTilePages; ++k) {
                 const uint32_t *s = &sv[k / 2][(k & 1) * 16];
-                float m0_ = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
-                float m1_ = fmax3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+                float u0 = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+                float u1 = fmax3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
 #pragma unroll
                 for (int x = 6; x < 14; x += 4) {
-                    m0_ = fmax3(m0_, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-                    m1_ = fmax3(m1_, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+                    u0 = fmax3(u0, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                    u1 = fmax3(u1, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
                 }
-                m0_ = fmax3(m0_, __uint_as_float(s[14]), __uint_as_float(s[15]));
-                tmax = fmaxf(tmax, fmaxf(m0_, m1_) * cs[k]);
+                u0 = fmax3(u0, __uint_as_float(s[14]), __uint_as_float(s[15]));
+                tmax = fmaxf(tmax, fmaxf(u0, u1) * cs[k]);
             }
             float m_new = m_used;
             if (tmax > m_used + kMaxSlack) m_new = tmax;
@@ -597,7 +679,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             // O holds the earlier tiles' sum under the old maximum and reference
             // scale.  S_j was issued after PV_{j-1} and completes after it.
             if (__any_sync(0xffffffffu, corr_o != 1.f) && j >= 1) {
-#pragma unroll
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {
                     uint32_t ov[16];
                     tmem_ld_32x32b_x16(tO + c0, ov);
@@ -614,14 +696,14 @@ kv8_tiles_kernel(const Kv8Params p) {
             // bf16 values carry no scale of their own: their weights take 1 / vref
             const float unscale = is_tail ? 1.f / vref : 1.f;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t pk[16];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int col = h * 32 + 2 * i;
-                    const float c = cs[col / 16];
+                for (int i = 0; i < 32; ++i) {
+                    const int col = h * 64 + 2 * i;
+                    const float f = cs[col / 16];
                     const uint64_t xa = f2_fma(f2_pack(__uint_as_float(sv[col / 32][col % 32]),
-                                                       __uint_as_float(sv[col / 32][col % 32 + 1])), f2_pack(c, c), base2);
+                                                       __uint_as_float(sv[col / 32][col % 32 + 1])), f2_pack(f, f), base2);
                     float u0, u1;
                     f2_unpack(xa, u0, u1);
                     u0 = fast_exp2(u0);
@@ -629,7 +711,7 @@ kv8_tiles_kernel(const Kv8Params p) {
                     ps2[i & 1] = f2_add(ps2[i & 1], f2_pack(u0, u1));
                     pk[i] = is_tail ? pack_bf16x2(u0 * unscale, u1 * unscale) : pack_f16(u0, u1);
                 }
-                tmem_st_32x32b_x16(tS + h * 16, pk);
+                tmem_st_32x32b_x32(tS + h * 32, pk);
             }
             float q0, q1, q2, q3;
             f2_unpack(ps2[0], q0, q1);
@@ -637,10 +719,10 @@ kv8_tiles_kernel(const Kv8Params p) {
             l = l * corr + ((q0 + q1) + (q2 + q3));
             m_used = m_new;
             tmem_st_wait();
-            // the next tile is bf16: so is Q from here on.  This group's S of the
+            // the next tile is bf16, and so is Q from here on: this group's S of the
             // last 8-bit tile is complete, and the next is issued after these
-            // warps' arrivals.
-            if (!is_tail && has_tail && j + 1 == n_pre) put_q(false);
+            // warps' arrivals
+            if (!is_tail && has_tail && j + 1 == n_pre) q_to_bf16();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[grp]);
