@@ -187,7 +187,7 @@ jsv_status jsv_accum_logp_tree(const float *logp, const int32_t *topk_tokens, co
 
 size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, const jsv_kv8 *cache8) {
     if (check_batch(batch) != JSV_OK || check_kv8(batch, cache8) != JSV_OK) return 0;
-    return jsv::attention_kv8_workspace_bytes(jsv::to_args(batch));
+    return jsv::attention_kv8_workspace_bytes(jsv::to_args(batch), *cache8);
 }
 
 jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
@@ -202,7 +202,7 @@ jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8,
         return JSV_ERR_INVALID_ARG;
     if (!(scale > 0.f) || scale > 3.0e38f) return JSV_ERR_INVALID_ARG;
     const jsv::BatchArgs a = jsv::to_args(batch);
-    const size_t need = jsv::attention_kv8_workspace_bytes(a);
+    const size_t need = jsv::attention_kv8_workspace_bytes(a, *cache8);
     if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 256)))) return JSV_ERR_INVALID_ARG;
     return from_cuda(jsv::launch_tree_attention_kv8(a, *cache8, q, k_cache, v_cache, scale, out, workspace,
                                                     static_cast<cudaStream_t>(stream)));

@@ -40,12 +40,18 @@ __device__ __forceinline__ bool load_request_kv8(const Kv8Params &p, int b, Requ
     return true;
 }
 
-// What a request's splits share out: its pages, or its 128-slot tiles (the
-// 8-bit pages' and, from the first bf16 slot on, the others').
+// What a request's splits share out: its pages, or its 128-slot tiles, of the
+// 8-bit pages and, from the first bf16 slot on, of the others, which count
+// twice (copied, masked, and Q brought back to bf16 for the first: about twice
+// the cycles).
 __device__ __forceinline__ int request_pages(const Request &r) { return (r.P + r.n + 15) / 16; }
 __device__ __forceinline__ int prefix_tiles(const Request &r) { return (r.P / 16 + 7) / 8; }
 __device__ __forceinline__ int request_units(const Kv8Params &p, const Request &r) {
-    return p.by_tiles ? prefix_tiles(r) + ((r.P & 15) + r.n + 127) / 128 : request_pages(r);
+    return p.by_tiles ? prefix_tiles(r) + 2 * (((r.P & 15) + r.n + 127) / 128) : request_pages(r);
+}
+// The tile that starts at a unit (in the middle of a bf16 tile: the next).
+__device__ __forceinline__ int unit_tile(int u, int pre_tiles) {
+    return u <= pre_tiles ? u : pre_tiles + (u - pre_tiles + 1) / 2;
 }
 // Splits of a request of `units`: about C units each, at most S.
 __device__ __forceinline__ int unit_splits(int units, int C, int S) { return max(1, min(S, (units + C - 1) / C)); }

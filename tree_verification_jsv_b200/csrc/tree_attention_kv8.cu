@@ -49,39 +49,53 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // Few rows: warps stream pages, each with a ring and an accumulator of its own
 // ---------------------------------------------------------------------------
 // With few query rows the work is reading the cache.  A CTA of four warps
-// takes (request, KV head, 16*MT packed query rows, split); its warps take the
+// takes (request, KV head, 8*NT packed query rows, split); its warps take the
 // split's pages in turn.  One lane keeps kRowStages pages of K and V in flight
 // into the warp's own ring (one swizzled 16 x D box each, so that the operand
 // reads below have no bank conflicts), and no warp waits for another before
 // the merge at the end.
 //
-// Register operands of mma.m16n8k16 straight from the codes, lane = 4 n + t:
-//   S = Q K^T   column n of tile j is key 8j + n; lane t supplies the dims
-//               t*D/4 .. of that key, four to a k-step, and of Q alike
-//   O += P V    the accumulator layout of S is the A operand layout of P;
-//               lane (t, n) reads keys 2t, 2t+1, 2t+8, 2t+9 at dims n*D/8 ..,
-//               pairs the keys' bytes, and tile i is dim n*D/8 + i for
-//               column n, which leaves each lane D/4 neighbouring dims of O
+// The products are taken transposed, so that the padding of the rows is to 8
+// (the MMA's N) and not to 16 (its M): one token of a model with four query
+// heads to a KV head has four rows.  Register operands of mma.m16n8k16
+// straight from the codes, lane = 4 n + t:
+//   S^T = K Q^T     A: keys n and n + 8 of the page; lane t supplies the dims
+//                   t*D/4 .. of its keys, four to a k-step, and of Q alike;
+//                   the result has keys n, n + 8 of rows 2t, 2t + 1
+//   O^T += V^T P^T  B: P as it comes from the exponentials, two 8 x 8 blocks
+//                   transposed in registers (movmatrix); A: lane (t, n) reads
+//                   keys 2t, 2t+1, 2t+8, 2t+9 at dims n*D/8 .. and pairs the
+//                   keys' bytes; rows n and n + 8 of tile i are dims
+//                   n*D/8 + 2i and + 2i + 1, so that a lane ends with D/8
+//                   neighbouring dims of rows 2t and 2t + 1
 constexpr int kRowWarps = 4;
-constexpr int kRowStages = 4;
+constexpr int kRowStages = 2;
 
-template <int D, int MT>
+template <int D, int NT>
 struct RowSmem {
     static constexpr int kBlock = 16 * D;                        // codes of one page and head
     static constexpr int kRing = kRowStages * 2 * kBlock;        // a warp's
-    static constexpr int kMerge = 16 * MT * D * 4;               // a warp's, over its ring
+    static constexpr int kMerge = 8 * NT * D * 4;                // a warp's, over its ring
     static constexpr int kWarp = kRing > kMerge ? kRing : kMerge;
     static constexpr int kTotal = kRowWarps * kWarp + 1024;
+    // CTAs an SM that the registers are to leave room for
+    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;
 };
 
-template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, RowSmem<D, NT>::kCtas)
 kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Kv8Params p) {
     pdl_allow_dependents();
-    using L = RowSmem<D, MT>;
-    constexpr int kRows = 16 * MT;
+    using L = RowSmem<D, NT>;
+    constexpr int kRows = 8 * NT;
     constexpr int kSteps = D / 16;               // k-steps of a score
-    constexpr int kTiles = D / 8;                // column tiles of the output
+    constexpr int kTiles = D / 16;               // 16-dim tiles of the output
     extern __shared__ uint8_t dsmem[];
     __shared__ __align__(8) uint64_t full[kRowWarps][kRowStages];
     __shared__ uint32_t anc[kRows][kTreeWords];
@@ -174,113 +188,102 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         __syncthreads();
     }
 
-    // Q rows n and n + 8 of each row tile, dims t*D/4 .., as bf16 pairs:
-    // words 2s, 2s+1 are k-step s.  Rows past the request are zero.
-    uint32_t qa[MT][kSteps][4];
+    // Q row n of each row tile, dims t*D/4 .., as bf16 pairs: words 2s, 2s+1
+    // are k-step s.  Rows past the request are zero.
+    uint32_t qb[NT][kSteps][2];
     auto load_q = [&]() {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const int rg = m0 + nt * 8 + n;
+            const size_t qi = ((size_t)(r.base + rg / G) * a.Hq + g * G + rg % G) * D + t * (D / 4);
+            const bool in = rg < rows_total && JSV_IN_BOUNDS(qi + D / 4 - 1, (long long)a.total_nodes * a.Hq * D,
+                                                             a.dev_status);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int rg = m0 + mt * 16 + hh * 8 + n;
-                const size_t qi = ((size_t)(r.base + rg / G) * a.Hq + g * G + rg % G) * D + t * (D / 4);
-                const bool in = rg < rows_total && JSV_IN_BOUNDS(qi + D / 4 - 1, (long long)a.total_nodes * a.Hq * D,
-                                                                 a.dev_status);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (in) w = __ldg(reinterpret_cast<const uint4 *>(p.q + qi) + c);
-                    qa[mt][2 * c][hh] = w.x;
-                    qa[mt][2 * c][hh + 2] = w.y;
-                    qa[mt][2 * c + 1][hh] = w.z;
-                    qa[mt][2 * c + 1][hh + 2] = w.w;
-                }
+            for (int c = 0; c < D / 32; ++c) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (in) w = __ldg(reinterpret_cast<const uint4 *>(p.q + qi) + c);
+                qb[nt][2 * c][0] = w.x;
+                qb[nt][2 * c][1] = w.y;
+                qb[nt][2 * c + 1][0] = w.z;
+                qb[nt][2 * c + 1][1] = w.w;
             }
+        }
     };
-    float fac[MT][2];                            // score to log2 units, before the K scale
+    float fac[NT][2];                            // rows 2t, 2t + 1: score to log2 units, before the K scale
     load_q();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt) {
+        // the row's largest magnitude to [2^13, 2^14)
+        uint32_t mx = 0;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            // the row's largest magnitude to [2^13, 2^14)
-            uint32_t mx = 0;
+        for (int s = 0; s < kSteps; ++s) mx = __vmaxu2(mx, __vmaxu2(qb[nt][s][0] & 0x7fff7fffu, qb[nt][s][1] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = min(max((int)(mx >> 7), 14), 254);    // biased exponent (255: not finite, stays so)
+        const float up = __uint_as_float((uint32_t)(267 - ex) << 23);
+        const float down = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
+        fac[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        fac[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-                mx = __vmaxu2(mx, __vmaxu2(qa[mt][s][hh] & 0x7fff7fffu, qa[mt][s][hh + 2] & 0x7fff7fffu));
-            mx = max(mx & 0xffffu, mx >> 16);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int ex = max((int)(mx >> 7), 14);              // biased exponent (255: not finite, stays so)
-            const float up = __uint_as_float((uint32_t)(267 - min(ex, 254)) << 23);
-            fac[mt][hh] = p.scale_log2 * __uint_as_float((uint32_t)(min(ex, 254) - 13) << 23);
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int k = hh; k < 4; k += 2) {
-                    const uint32_t w = qa[mt][s][k];
-                    qa[mt][s][k] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                }
-        }
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w = qb[nt][s][k];
+                qb[nt][s][k] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+            }
+    }
 
-    float o[MT][kTiles][4], m[MT][2], l[MT][2], vref = 0.f;
+    // o[nt][i][c + 2 d]: row 2t + c, dim n*D/8 + 2i + d
+    float o[NT][kTiles][4], m[NT][2], l[NT][2], vref = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
-        m[mt][0] = m[mt][1] = -INFINITY;
-        l[mt][0] = l[mt][1] = 0.f;
+            for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
     }
-    auto scale_o = [&](int mt, int hh, float f) {
+    auto scale_o = [&](int nt, int c, float f) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            o[mt][i][2 * hh] *= f;
-            o[mt][i][2 * hh + 1] *= f;
+            o[nt][i][c] *= f;
+            o[nt][i][c + 2] *= f;
         }
     };
-    // Scores in log2 units (sc[mt][j][2 hh + c]: row n + 8 hh, key 8 j + 2 t + c;
-    // -inf: not seen) to weights, with the running maximum and sum.
-    auto softmax = [&](float (&sc)[MT][2][4]) {
+    // Scores in log2 units (sc[nt][c + 2 h]: row 2t + c, key n + 8 h; -inf: not
+    // seen) to weights, with the running maximum and sum.
+    auto softmax = [&](float (&sc)[NT][4]) {
         bool grow = false;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const float mx = fmaxf(fmaxf(sc[mt][0][2 * hh], sc[mt][0][2 * hh + 1]),
-                                       fmaxf(sc[mt][1][2 * hh], sc[mt][1][2 * hh + 1]));
-                grow |= mx > m[mt][hh] + kMaxSlack;
-            }
+            for (int c = 0; c < 2; ++c) grow |= fmaxf(sc[nt][c], sc[nt][c + 2]) > m[nt][c] + kMaxSlack;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    float mx = fmaxf(fmaxf(sc[mt][0][2 * hh], sc[mt][0][2 * hh + 1]),
-                                     fmaxf(sc[mt][1][2 * hh], sc[mt][1][2 * hh + 1]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    if (mx > m[mt][hh] + kMaxSlack) {
-                        const float corr = fast_exp2(m[mt][hh] - mx);        // 0 from -inf
-                        scale_o(mt, hh, corr);
-                        l[mt][hh] *= corr;
-                        m[mt][hh] = mx;
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(sc[nt][c], sc[nt][c + 2]);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    if (mx > m[nt][c] + kMaxSlack) {
+                        const float corr = fast_exp2(m[nt][c] - mx);         // 0 from -inf
+                        scale_o(nt, c, corr);
+                        l[nt][c] *= corr;
+                        m[nt][c] = mx;
                     }
                 }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const float base = m[mt][hh] == -INFINITY ? 0.f : m[mt][hh];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 2 * hh; k < 2 * hh + 2; ++k) {
-                        sc[mt][j][k] = fast_exp2(sc[mt][j][k] - base);
-                        l[mt][hh] += sc[mt][j][k];
-                    }
+            for (int c = 0; c < 2; ++c) {
+                const float base = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+                sc[nt][c] = fast_exp2(sc[nt][c] - base);
+                sc[nt][c + 2] = fast_exp2(sc[nt][c + 2] - base);
+                l[nt][c] += sc[nt][c] + sc[nt][c + 2];
             }
     };
     // the reference scale takes in a page's (or, for bf16 values, 1)
@@ -288,13 +291,13 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (fabsf(vs) > 2.f * vref) {
             const float f = vref / fabsf(vs);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                scale_o(mt, 0, f);
-                scale_o(mt, 1, f);
+            for (int nt = 0; nt < NT; ++nt) {
+                scale_o(nt, 0, f);
+                scale_o(nt, 1, f);
             }
             vref = fabsf(vs);
         }
-        return vref > 0.f ? vs / vref * kWeightShift : vs * 0.f;
+        return vref > 0.f ? __fdividef(vs, vref) * kWeightShift : vs * 0.f;
     };
 
     bool ok = true;
@@ -316,51 +319,42 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         const uint8_t *sk = ring + st * 2 * L::kBlock, *sv = sk + L::kBlock;
 
-        float sc[MT][2][4];
+        float sc[NT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int k = 0; k < 4; ++k) sc[nt][k] = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sc[mt][j][k] = 0.f;
+        for (int c = 0; c < D / 64; ++c) {
+            uint32_t kw[2][4];                   // keys n, n + 8
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
+            for (int j = 0; j < 2; ++j) {
                 const int at = D == 128 ? (8 * j + n) * 128 + (((2 * t + c) ^ n) << 4)
                                         : (8 * j + n) * 64 + ((t ^ (n >> 1)) << 4);
                 const uint4 w = *reinterpret_cast<const uint4 *>(sk + at);
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                kw[j][0] = w.x, kw[j][1] = w.y, kw[j][2] = w.z, kw[j][3] = w.w;
+            }
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    uint32_t b0, b1;
-                    codes_to_f16<FMT>(ws[s], b0, b1);
+            for (int s = 0; s < 4; ++s) {
+                uint32_t ka[4];
+                codes_to_f16<FMT>(kw[0][s], ka[0], ka[2]);
+                codes_to_f16<FMT>(kw[1][s], ka[1], ka[3]);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][j], qa[mt][4 * c + s], b0, b1);
-                }
+                for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], ka, qb[nt][4 * c + s][0], qb[nt][4 * c + s][1]);
             }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const float f = fac[mt][hh] * ks;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    sc[mt][j][2 * hh] *= f;
-                    sc[mt][j][2 * hh + 1] *= f;
-                }
-            }
+            for (int k = 0; k < 4; ++k) sc[nt][k] *= fac[nt][k & 1] * ks;
         softmax(sc);
         const float pv = take_scale(vs);
-        uint32_t pa[MT][4];
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            pa[mt][0] = pack_f16(sc[mt][0][0] * pv, sc[mt][0][1] * pv);
-            pa[mt][1] = pack_f16(sc[mt][0][2] * pv, sc[mt][0][3] * pv);
-            pa[mt][2] = pack_f16(sc[mt][1][0] * pv, sc[mt][1][1] * pv);
-            pa[mt][3] = pack_f16(sc[mt][1][2] * pv, sc[mt][1][3] * pv);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pb[nt][h] = transpose_8x8(pack_f16(sc[nt][2 * h] * pv, sc[nt][2 * h + 1] * pv));
         uint32_t vw[4][D / 32];                  // keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -378,14 +372,13 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                // dims 4c + 2 half and the next, of keys (2t, 2t+1) and (2t+8, 2t+9)
                 const uint32_t sel = half ? 0x7362 : 0x5140;
-                uint32_t b0[2], b1[2];
-                codes_to_f16<FMT>(__byte_perm(vw[0][c], vw[1][c], sel), b0[0], b0[1]);
-                codes_to_f16<FMT>(__byte_perm(vw[2][c], vw[3][c], sel), b1[0], b1[1]);
+                uint32_t va[4];
+                codes_to_f16<FMT>(__byte_perm(vw[0][c], vw[1][c], sel), va[0], va[1]);
+                codes_to_f16<FMT>(__byte_perm(vw[2][c], vw[3][c], sel), va[2], va[3]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * c + 2 * half + u], pa[mt], b0[u], b1[u]);
+                for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * c + half], va, pb[nt][0], pb[nt][1]);
             }
         __syncwarp();
         if (i + kRowStages < count) issue(i + kRowStages, grp);
@@ -413,29 +406,29 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const size_t row0 = (size_t)page * 16 * a.Hkv + g;       // row of slot 0, in heads
             const long long elems = (long long)a.num_pages * 16 * a.Hkv * D;
             const int slots = min(16, r.P + r.n - lp * 16);          // slots that hold anything
-            float sc[MT][2][4];
+            float sc[NT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int k = 0; k < 4; ++k) sc[nt][k] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[mt][j][k] = 0.f;
+            for (int c = 0; c < D / 32; ++c) {
+                uint4 kw[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const size_t ki = (row0 + (size_t)(8 * j + n) * a.Hkv) * D + t * (D / 4);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint4 w = make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 2; ++j) {
+                    const size_t ki = (row0 + (size_t)(8 * j + n) * a.Hkv) * D + t * (D / 4);
+                    kw[j] = make_uint4(0, 0, 0, 0);
                     if (8 * j + n < slots && JSV_IN_BOUNDS(ki + c * 8 + 7, elems, a.dev_status))
-                        w = *(reinterpret_cast<const uint4 *>(p.k + ki) + c);
+                        kw[j] = *(reinterpret_cast<const uint4 *>(p.k + ki) + c);
+                }
+                const uint32_t k0[4] = {kw[0].x, kw[1].x, kw[0].y, kw[1].y}, k1[4] = {kw[0].z, kw[1].z, kw[0].w, kw[1].w};
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma_bf16(sc[mt][j], qa[mt][2 * c], w.x, w.y);
-                        mma_bf16(sc[mt][j], qa[mt][2 * c + 1], w.z, w.w);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_bf16(sc[nt], k0, qb[nt][2 * c][0], qb[nt][2 * c][1]);
+                    mma_bf16(sc[nt], k1, qb[nt][2 * c + 1][0], qb[nt][2 * c + 1][1]);
                 }
             }
-            uint32_t vw[4][D / 16], key_bad = 0;                     // bit k: key k holds a non-finite value
+            uint32_t vw[4][D / 16], key_bad = 0;                     // bit k: key k of the page is not finite
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int key = 2 * t + (k & 1) + (k & 2) * 4;
@@ -450,53 +443,42 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 uint32_t top = 0;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) top = __vmaxu2(top, vw[k][c] & 0x7fff7fffu);
-                if (max(top & 0xffffu, top >> 16) >= 0x7f80u) key_bad |= 1u << k;
+                if (max(top & 0xffffu, top >> 16) >= 0x7f80u) key_bad |= 1u << key;
             }
             // a weight of zero does not undo an infinity or NaN in the product:
             // such a key's values are taken out, and a row that sees it gets
             // NaN through its sum
-            if (__any_sync(0xffffffffu, key_bad)) {
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) key_bad |= __shfl_xor_sync(0xffffffffu, key_bad, off);
+            key_bad = __reduce_or_sync(0xffffffffu, key_bad);
+            if (key_bad) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if ((key_bad >> k) & 1)
+                    if ((key_bad >> (2 * t + (k & 1) + (k & 2) * 4)) & 1)
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) vw[k][c] = 0;
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int row = mt * 16 + hh * 8 + n;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int key = 2 * t + (k & 1) + (k & 2) * 4, node = lp * 16 + key - r.P;
-                        const bool seen = key < slots && (node < 0 || ((anc[row][node >> 5] >> (node & 31)) & 1u));
-                        float &s = sc[mt][k >> 1][2 * hh + (k & 1)];
-                        s = seen ? s * p.scale_log2 : -INFINITY;
-                        if (seen && ((key_bad >> k) & 1)) l[mt][hh] = __uint_as_float(0x7fc00000u);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int row = nt * 8 + 2 * t + (k & 1), key = n + (k & 2) * 4, node = lp * 16 + key - r.P;
+                    const bool seen = key < slots && (node < 0 || ((anc[row][node >> 5] >> (node & 31)) & 1u));
+                    sc[nt][k] = seen ? sc[nt][k] * p.scale_log2 : -INFINITY;
+                    if (seen && ((key_bad >> key) & 1)) l[nt][k & 1] = __uint_as_float(0x7fc00000u);
                 }
             softmax(sc);
             const float pv = take_scale(1.f);
-            uint32_t pa[MT][4];
+            uint32_t pb[NT][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                pa[mt][0] = pack_bf16x2(sc[mt][0][0] * pv, sc[mt][0][1] * pv);
-                pa[mt][1] = pack_bf16x2(sc[mt][0][2] * pv, sc[mt][0][3] * pv);
-                pa[mt][2] = pack_bf16x2(sc[mt][1][0] * pv, sc[mt][1][1] * pv);
-                pa[mt][3] = pack_bf16x2(sc[mt][1][2] * pv, sc[mt][1][3] * pv);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pb[nt][h] = transpose_8x8(pack_bf16x2(sc[nt][2 * h] * pv, sc[nt][2 * h + 1] * pv));
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
+                const uint32_t va[4] = {__byte_perm(vw[0][c], vw[1][c], 0x5410), __byte_perm(vw[0][c], vw[1][c], 0x7632),
+                                        __byte_perm(vw[2][c], vw[3][c], 0x5410), __byte_perm(vw[2][c], vw[3][c], 0x7632)};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(vw[0][c], vw[1][c], sel), b1 = __byte_perm(vw[2][c], vw[3][c], sel);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma_bf16(o[mt][2 * c + half], pa[mt], b0, b1);
-                }
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][c], va, pb[nt][0], pb[nt][1]);
             }
         }
     }
@@ -506,26 +488,21 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     float *mine = reinterpret_cast<float *>(ring);
     __syncwarp();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int row = mt * 16 + hh * 8 + n;
-            float sum = l[mt][hh];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (t == 0) {
-                m_sh[warp][row] = ok ? m[mt][hh] : -INFINITY;
+        for (int c = 0; c < 2; ++c) {
+            const int row = nt * 8 + 2 * t + c;
+            float sum = l[nt][c];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (n == 0) {
+                m_sh[warp][row] = ok ? m[nt][c] : -INFINITY;
                 l_sh[warp][row] = ok ? sum : 0.f;
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < kTiles; i += 4) {
-                    float4 v = make_float4(o[mt][i][2 * hh + c], o[mt][i + 1][2 * hh + c], o[mt][i + 2][2 * hh + c],
-                                           o[mt][i + 3][2 * hh + c]);
-                    v.x *= undo, v.y *= undo, v.z *= undo, v.w *= undo;
-                    *reinterpret_cast<float4 *>(mine + row * D + (2 * t + c) * kTiles + i) = v;
-                }
+            for (int i = 0; i < kTiles; i += 2)
+                *reinterpret_cast<float4 *>(mine + row * D + n * (D / 8) + 2 * i) =
+                    make_float4(o[nt][i][c] * undo, o[nt][i][c + 2] * undo, o[nt][i + 1][c] * undo, o[nt][i + 1][c + 2] * undo);
         }
     __syncthreads();
     const size_t rows = (size_t)a.total_nodes * a.Hq;
@@ -570,7 +547,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 constexpr int kMergeWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32, 16)
+__global__ void __launch_bounds__(kMergeWarps * 32, 8)
 kv8_merge_kernel(const Kv8Params p) {
     pdl_allow_dependents();
     pdl_wait_predecessor();
@@ -611,17 +588,32 @@ kv8_merge_kernel(const Kv8Params p) {
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
     constexpr int kPer = D / 32;
     float o[kPer] = {};
-#pragma unroll 4
-    for (int s = 0; s < S; ++s) {
-        const float w = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
-        if (w == 0.f) continue;
-        const float *po = p.ws_o + ((size_t)s * rows + row_id) * D + lane * kPer;
-        if constexpr (kPer == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(po);
-            o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]), o[3] = fmaf(w, v.w, o[3]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(po);
-            o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]);
+    // eight splits' loads in flight at a time: no branch on a weight between
+    // them (every split of the request has written its row)
+    const float *po = p.ws_o + row_id * D + lane * kPer;
+    for (int s0 = 0; s0 < S; s0 += 8) {
+        float v[8][kPer];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) v[i][x] = 0.f;
+            if (s0 + i < S) {
+                const float *at = po + (size_t)(s0 + i) * rows * D;
+                if constexpr (kPer == 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(at);
+                    v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
+                } else {
+                    const float2 w = *reinterpret_cast<const float2 *>(at);
+                    v[i][0] = w.x, v[i][1] = w.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int s = s0 + i;
+            const float w = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) o[x] = w == 0.f ? o[x] : fmaf(w, v[i][x], o[x]);
         }
     }
     const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
@@ -640,55 +632,64 @@ namespace {
 constexpr int kRowsFormMost = 32;
 
 struct Kv8Plan {
-    int mt;                                      // row tiles of a warp, 0: the tcgen05 form
+    int nt;                                      // 8-row tiles of a warp, 0: the tcgen05 form
     int S, C;
 };
 
-// Splits that minimise waves * (fixed + units of a split) + what a split's
-// partial costs, in units' times; the estimate takes every request for the
-// largest the batch may hold.
-void choose_splits(Kv8Plan &pl, long long units_of_work, int total, int most, int slots, int per_unit, double fixed,
-                   double merge, double per_split) {
+// Splits of the largest request that minimise waves * (fixed + its share of
+// the units) + what a split's partial costs, in units' times.  `load`: how
+// much of B requests of the largest size the batch can hold (shorter requests
+// take fewer splits, the last of them not whole).
+void choose_splits(Kv8Plan &pl, long long ctas, double load, int total, int most, int slots, int per_unit,
+                   double fixed, double merge, double per_split) {
     double best = 1e300;
     pl.S = 1;
     for (int s = 1; s <= kMaxSplits && s <= most; ++s) {
-        const long long waves = (units_of_work * s + slots - 1) / slots;
-        const double cost = (double)waves * (fixed + (double)((total + s * per_unit - 1) / (s * per_unit))) +
+        const double n = (double)ctas * (load < 1.0 ? std::min(s * load + 0.5, (double)s) : s);
+        const long long waves = (long long)((n + slots - 1) / slots);
+        const double cost = (double)std::max(waves, 1ll) * (fixed + (double)((total + s * per_unit - 1) / (s * per_unit))) +
                             (s > 1 ? merge + per_split * s : 0.0);
         if (cost < best - 1e-9) best = cost, pl.S = s;
     }
     pl.C = (total + pl.S - 1) / pl.S;
 }
 
-Kv8Plan plan_of(const BatchArgs &a) {
+// From the host-side fields: the largest request's bounds, and the pages that
+// there are for all of them.
+Kv8Plan plan_of(const BatchArgs &a, const jsv_kv8 &c) {
     Kv8Plan pl;
     const int rows = a.max_nodes * (a.Hq / a.Hkv);
     const int sms = std::max(device_sm_count(), 1);
+    const double load = std::min(1.0, ((double)c.num_pages + a.B) / ((double)a.B * (a.max_prefix / 16 + 1)));
     if (rows <= kRowsFormMost) {
-        pl.mt = rows <= 16 ? 1 : 2;
-        const int tiles = (rows + 16 * pl.mt - 1) / (16 * pl.mt);
+        pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+        const int tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
         const int total = (int)(((long long)a.max_prefix + a.max_nodes + 15) / 16);
-        choose_splits(pl, (long long)a.B * a.Hkv * tiles, total, std::max(total / kRowWarps, 1),
-                      sms * (pl.mt == 1 ? 3 : 2), kRowWarps, 8.0, 4.0, 0.05);
+        // a warp takes about 0.4 us (8 rows) to 0.9 us (32) for a page
+        choose_splits(pl, (long long)a.B * a.Hkv * tiles, load, total, std::max(total / kRowWarps, 1),
+                      sms * (pl.nt == 1 ? 4 : pl.nt == 2 ? 3 : 2), kRowWarps, 8.0, 4.0, 0.05);
     } else {
-        pl.mt = 0;
+        pl.nt = 0;
         const int tiles = (rows + 255) / 256;
-        const int total = (int)(((long long)a.max_prefix / 16 + 7) / 8) + (15 + a.max_nodes + 127) / 128;
-        // a tile takes about 2.1 us; a split's fp32 partial is written and read at about 6 TB/s
-        const double per_split = (double)a.total_nodes * a.Hq * (a.D + 2) * 8.0 / 6.0e6 / 2.1;
-        choose_splits(pl, (long long)a.B * a.Hkv * tiles, total, total, sms, 1, 3.0, 1.0, per_split);
+        const int total = (int)(((long long)a.max_prefix / 16 + 7) / 8) + 2 * ((15 + a.max_nodes + 127) / 128);
+        // a tile takes about 2.3 us, 1.7 us where the groups share out the
+        // tiles; a split's fp32 partial is written and read at about 6 TB/s
+        const double tile_us = rows <= 128 ? 1.7 : 2.3;
+        const double per_split = (double)a.total_nodes * a.Hq * (a.D + 2) * 8.0 / 6.0e6 / tile_us;
+        choose_splits(pl, (long long)a.B * a.Hkv * tiles, load, total, total, sms, 1, 9.0 / tile_us, 4.0 / tile_us,
+                      per_split);
     }
     return pl;
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int NT>
 cudaError_t launch_rows(const Kv8Params &p, cudaStream_t st) {
-    using L = RowSmem<D, MT>;
+    using L = RowSmem<D, NT>;
     CUtensorMap tmK, tmV;
     const uint64_t rows = (uint64_t)p.c.num_pages * p.a.Hkv * 16;
     if (!encode_tensor_map_u8_2d(&tmK, p.c.k, D, rows, 16) || !encode_tensor_map_u8_2d(&tmV, p.c.v, D, rows, 16))
         return cudaErrorInvalidValue;
-    auto kernel = kv8_rows_kernel<D, FMT, MT>;
+    auto kernel = kv8_rows_kernel<D, FMT, NT>;
     static PerDeviceOnce once;
     cudaError_t e = once.run([&]() {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
@@ -699,21 +700,24 @@ cudaError_t launch_rows(const Kv8Params &p, cudaStream_t st) {
     });
     if (e != cudaSuccess) return e;
     const int G = p.a.Hq / p.a.Hkv;
-    dim3 grid((p.a.max_nodes * G + 16 * MT - 1) / (16 * MT), p.S, p.a.B * p.a.Hkv);
+    dim3 grid((p.a.max_nodes * G + 8 * NT - 1) / (8 * NT), p.S, p.a.B * p.a.Hkv);
     e = launch_pdl(kernel, grid, dim3(kRowWarps * 32), L::kTotal, st, tmK, tmV, p);
     count_launches(1);
     return e;
 }
 
+template <int D, int FMT>
+cudaError_t launch_rows(const Kv8Params &p, int nt, cudaStream_t st) {
+    return nt == 1 ? launch_rows<D, FMT, 1>(p, st) : nt == 2 ? launch_rows<D, FMT, 2>(p, st) : launch_rows<D, FMT, 4>(p, st);
+}
+
 template <int D>
-cudaError_t launch_kv8(const Kv8Params &p, int mt, cudaStream_t st) {
+cudaError_t launch_kv8(const Kv8Params &p, int nt, cudaStream_t st) {
     cudaError_t e;
-    if (mt == 0)
+    if (nt == 0)
         e = launch_kv8_tiles(p, st);
-    else if (p.c.format == JSV_KV8_E4M3)
-        e = mt == 1 ? launch_rows<D, JSV_KV8_E4M3, 1>(p, st) : launch_rows<D, JSV_KV8_E4M3, 2>(p, st);
     else
-        e = mt == 1 ? launch_rows<D, JSV_KV8_INT8, 1>(p, st) : launch_rows<D, JSV_KV8_INT8, 2>(p, st);
+        e = p.c.format == JSV_KV8_E4M3 ? launch_rows<D, JSV_KV8_E4M3>(p, nt, st) : launch_rows<D, JSV_KV8_INT8>(p, nt, st);
     if (e != cudaSuccess || p.S == 1) return e;
     static PerDeviceOnce once;
     e = prefer_max_shared(kv8_merge_kernel<D>, once);
@@ -727,15 +731,15 @@ cudaError_t launch_kv8(const Kv8Params &p, int mt, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_kv8_workspace_bytes(const BatchArgs &a) {
-    const Kv8Plan pl = plan_of(a);
+size_t attention_kv8_workspace_bytes(const BatchArgs &a, const jsv_kv8 &c) {
+    const Kv8Plan pl = plan_of(a, c);
     return pl.S > 1 ? (size_t)pl.S * a.total_nodes * a.Hq * ((size_t)a.D + 2) * sizeof(float) : 0;
 }
 
 cudaError_t launch_tree_attention_kv8(const BatchArgs &a, const jsv_kv8 &c, const uint16_t *q,
                                       const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,
                                       void *ws, cudaStream_t st) {
-    const Kv8Plan pl = plan_of(a);
+    const Kv8Plan pl = plan_of(a, c);
     Kv8Params p;
     p.a = a;
     p.c = c;
@@ -746,10 +750,10 @@ cudaError_t launch_tree_attention_kv8(const BatchArgs &a, const jsv_kv8 &c, cons
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = pl.S;
     p.C = pl.C;
-    p.by_tiles = pl.mt == 0;
+    p.by_tiles = pl.nt == 0;
     p.ws_o = pl.S > 1 ? static_cast<float *>(ws) : nullptr;
     p.ws_ml = pl.S > 1 ? p.ws_o + (size_t)pl.S * a.total_nodes * a.Hq * a.D : nullptr;
-    return a.D == 128 ? launch_kv8<128>(p, pl.mt, st) : launch_kv8<64>(p, pl.mt, st);
+    return a.D == 128 ? launch_kv8<128>(p, pl.nt, st) : launch_kv8<64>(p, pl.nt, st);
 }
 
 }  // namespace jsv

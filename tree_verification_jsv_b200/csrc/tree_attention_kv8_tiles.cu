@@ -4,8 +4,12 @@
 //
 // One CTA per (request, KV head, 256 packed query rows, split); the rows form
 // two 128-row groups that take turns on the tensor core, as in
-// tree_attention.cu, whose MMA order and softmax this kernel keeps.  What
-// differs is where the operands come from: the codes are read by ordinary
+// tree_attention.cu, whose MMA order and softmax this kernel keeps.  Where a
+// CTA has 128 rows or fewer, both groups take the same rows and every other
+// tile each, and their results are merged at the end: one group alone would
+// leave the tensor core idle during its softmax (16 requests of 16 nodes over
+// 4096 tokens: 88 us with one group).  Also different is where the operands
+// come from: the codes are read by ordinary
 // 16-byte loads and written to the operand tiles as fp16 by seven converting
 // warps, one 128-key tile ahead, so the tensor core, the softmax and the
 // conversion run side by side.
@@ -48,20 +52,21 @@ constexpr int kKTeam = 3;
 constexpr int kMmaWarp = 4;
 constexpr int kSoftmaxWarp0 = 8;
 constexpr int kTileThreads = 512;
-// registers a thread after the split, of 128 at launch: 48 + 48 + 2 * 208 =
+// registers a thread after the split, of 128 at launch: 80 + 80 + 2 * 176 =
 // 4 * 128 over the four warpgroups
-constexpr int kRegsConv = 48;
-constexpr int kRegsMma = 48;
-constexpr int kRegsSoftmax = 208;
+constexpr int kRegsConv = 80;
+constexpr int kRegsMma = 80;
+constexpr int kRegsSoftmax = 176;
 constexpr int kSlots = 4;                        // tiles whose scales are held, see TileInfo
 constexpr float kWeightLog2 = 6.f;               // weights are held as 2^6 e: e <= 2^8 stays inside fp16
 
 // What the softmax warps need of a tile.  Written before the tile's K is
-// handed over; the slot of tile j is rewritten for tile j + 4, whose K tile
-// cannot start before every softmax warp is past tile j.
+// handed over and once its place in the ring is free: by then S of tile j - 2
+// is complete, which was issued after P of tile j - 4 arrived, so the slot's
+// last tile has been read.
 struct __align__(16) TileInfo {
     float ks[kTilePages];                        // read as two float4
-    float vref, vratio;                          // reference scale, and the previous one over it
+    float vref;                                  // reference scale of V
     // bf16 slots whose V row is not finite, as each converting warp found them
     uint32_t bad[kVTeam][kTileKeys / 32];
 };
@@ -84,8 +89,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 // The MMA issuer, one thread; see attention_mma_loop in tree_attention.cu for
 // the order and for why everything is a constant offset from a base.  Tiles
-// before `n_pre` are fp16, the others bf16.
-template <int D, int NG>
+// before `n_pre` are fp16, the others bf16.  kDual: group j % 2 takes tile j,
+// and S of its next tile, j + 2, follows PV of tile j; else both groups take
+// every tile.
+template <int D, bool kDual>
 __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_t aKV, int ntiles, int n_pre,
                                              uint64_t *k_full, uint64_t *v_full, uint64_t *k_empty, uint64_t *v_empty,
                                              uint64_t *s_full, uint64_t *p_full, uint64_t *o_done, uint64_t *q_ready,
@@ -138,29 +145,52 @@ __device__ __forceinline__ void kv8_mma_loop(uint32_t tmem, uint32_t aQ, uint32_
     if (ok) {
         tc_fence_after();
         issue_s(G0{}, n_pre > 0, dK0);
-        if constexpr (NG > 1) issue_s(G1{}, n_pre > 0, dK0);
+        if constexpr (!kDual) issue_s(G1{}, n_pre > 0, dK0);
         mma_commit(&k_empty[0]);
     }
-    for (int j = 0; ok && j < ntiles; ++j) {
-        asm volatile("" : "+l"(dQ), "+l"(dK0), "+l"(dV0));
-        const int st = j % kStages, stn = (j + 1) % kStages;
-        const uint32_t ph = (uint32_t)((j / kStages) & 1), phn = (uint32_t)(((j + 1) / kStages) & 1);
-        const bool more = j + 1 < ntiles;
-        const uint64_t dv = dV0 + st * kStageStep, dkn = dK0 + stn * kStageStep;
-        const uint32_t acc_first = j > 0 ? 1u : 0u;
-        const bool codes = j < n_pre, codes_n = j + 1 < n_pre;
-        ok = mbar_wait(&v_full[st], ph, abort_sh) && (!more || mbar_wait(&k_full[stn], phn, abort_sh));
-        if (!ok) break;
-        ok = mbar_wait(&p_full[0], j & 1, abort_sh);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(G0{}, codes, dv, acc_first);
-        if constexpr (NG == 1) mma_commit(&v_empty[st]);
-        if (more) {
-            issue_s(G0{}, codes_n, dkn);
-            if constexpr (NG == 1) mma_commit(&k_empty[stn]);
+    if constexpr (kDual) {
+        if (ok && ntiles > 1) {
+            ok = mbar_wait(&k_full[1], 0, abort_sh);
+            if (ok) {
+                tc_fence_after();
+                issue_s(G1{}, n_pre > 1, dK0 + kStageStep);
+                mma_commit(&k_empty[1]);
+            }
         }
-        if constexpr (NG > 1) {
+        auto turn = [&](auto grp_c, int j) -> bool {
+            constexpr int grp = decltype(grp_c)::value;
+            asm volatile("" : "+l"(dQ), "+l"(dK0), "+l"(dV0));
+            const uint32_t ph = (uint32_t)((j / 2) & 1);
+            const bool more = j + 2 < ntiles;
+            if (!mbar_wait(&v_full[grp], ph, abort_sh) || (more && !mbar_wait(&k_full[grp], ph ^ 1, abort_sh)) ||
+                !mbar_wait(&p_full[grp], ph, abort_sh))
+                return false;
+            tc_fence_after();
+            issue_pv(grp_c, j < n_pre, dV0 + grp * kStageStep, j > 1 ? 1u : 0u);
+            mma_commit(&v_empty[grp]);
+            if (more) {
+                issue_s(grp_c, j + 2 < n_pre, dK0 + grp * kStageStep);
+                mma_commit(&k_empty[grp]);
+            }
+            return true;
+        };
+        for (int j = 0; ok && j < ntiles; j += 2) ok = turn(G0{}, j) && (j + 1 >= ntiles || turn(G1{}, j + 1));
+    } else {
+        for (int j = 0; ok && j < ntiles; ++j) {
+            asm volatile("" : "+l"(dQ), "+l"(dK0), "+l"(dV0));
+            const int st = j % kStages, stn = (j + 1) % kStages;
+            const uint32_t ph = (uint32_t)((j / kStages) & 1), phn = (uint32_t)(((j + 1) / kStages) & 1);
+            const bool more = j + 1 < ntiles;
+            const uint64_t dv = dV0 + st * kStageStep, dkn = dK0 + stn * kStageStep;
+            const uint32_t acc_first = j > 0 ? 1u : 0u;
+            const bool codes = j < n_pre, codes_n = j + 1 < n_pre;
+            ok = mbar_wait(&v_full[st], ph, abort_sh) && (!more || mbar_wait(&k_full[stn], phn, abort_sh));
+            if (!ok) break;
+            ok = mbar_wait(&p_full[0], j & 1, abort_sh);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(G0{}, codes, dv, acc_first);
+            if (more) issue_s(G0{}, codes_n, dkn);
             ok = mbar_wait(&p_full[1], j & 1, abort_sh);
             if (!ok) break;
             tc_fence_after();
@@ -187,7 +217,6 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
 kv8_tiles_kernel(const Kv8Params p) {
     pdl_allow_dependents();
-    pdl_wait_predecessor();
     using L = TileSmem<D>;
     extern __shared__ uint8_t dsmem[];
     __shared__ __align__(8) uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
@@ -201,24 +230,6 @@ kv8_tiles_kernel(const Kv8Params p) {
     const int G = a.Hq / a.Hkv;
     const int b = blockIdx.z / a.Hkv, g = blockIdx.z % a.Hkv, split = blockIdx.y;
     const int m0 = blockIdx.x * kRowsPerCta;
-    Request r;
-    if (!load_request_kv8(p, b, r)) return;
-    const int rows_total = r.n * G;
-    if (m0 >= rows_total) return;
-    const int rows_here = min(kRowsPerCta, rows_total - m0);
-    const int ngroups = rows_here > kGroupRows ? 2 : 1;
-
-    // this split's tiles: n_pre of codes, then bf16 ones
-    const int pre_tiles = prefix_tiles(r), total = request_units(p, r), pages8 = r.P / 16;
-    const int Sb = unit_splits(total, p.C, p.S);
-    if (split >= Sb) return;
-    const int t_begin = (int)((long long)total * split / Sb), t_end = (int)((long long)total * (split + 1) / Sb);
-    const int ntiles = t_end - t_begin;
-    const int n_pre = max(0, min(t_end, pre_tiles) - t_begin);
-    const bool has_tail = n_pre < ntiles;
-    const int P0 = pages8 * 16;                  // first slot of the bf16 tiles
-    auto tail_slot = [&](int j) { return P0 + (t_begin + j - pre_tiles) * kTileKeys; };
-
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sKV = smem + L::kQ, *raw = sKV + kStages * L::kStage;
     // the request's parents, over the second V tile until the ancestors are found
@@ -244,6 +255,26 @@ kv8_tiles_kernel(const Kv8Params p) {
         abort_sh = 0;
         fence_barrier_init();
     }
+    pdl_wait_predecessor();
+    Request r;
+    if (!load_request_kv8(p, b, r)) return;
+    const int rows_total = r.n * G;
+    if (m0 >= rows_total) return;
+    const int rows_here = min(kRowsPerCta, rows_total - m0);
+    const bool dual = rows_here <= kGroupRows;
+
+    // this split's tiles: n_pre of codes, then bf16 ones
+    const int pre_tiles = prefix_tiles(r), total = request_units(p, r), pages8 = r.P / 16;
+    const int Sb = unit_splits(total, p.C, p.S);
+    if (split >= Sb) return;
+    const int t_begin = unit_tile((int)((long long)total * split / Sb), pre_tiles);
+    const int t_end = unit_tile((int)((long long)total * (split + 1) / Sb), pre_tiles);
+    const int ntiles = t_end - t_begin;
+    const int n_pre = max(0, min(t_end, pre_tiles) - t_begin);
+    const bool has_tail = n_pre < ntiles;
+    const int P0 = pages8 * 16;                  // first slot of the bf16 tiles
+    auto tail_slot = [&](int j) { return P0 + (t_begin + j - pre_tiles) * kTileKeys; };
+
     if (warp == kMmaWarp) {
         tmem_alloc(&tmem_base_sh, 512);
         tmem_relinquish();
@@ -263,8 +294,8 @@ kv8_tiles_kernel(const Kv8Params p) {
         // come as one bulk copy each into the warp's own part of `raw`, one tile
         // ahead: no warp waits for another, and the loop over pages is short and
         // rolled, so that it and the softmax's code fit the instruction caches
-        // together.  (Codes copied by every lane, or held in registers, which
-        // the softmax then lacks: 6-20% slower.)
+        // together (unrolled it is 13% slower on 256 nodes over 16384 tokens;
+        // codes copied by every lane or held in registers: 6-20%).
         // The page is read and stored in units of 512 bytes, 16 bytes a lane (4
         // rows at D = 128, 8 at D = 64).  Of eight neighbouring lanes four take
         // half a row of 128 bytes and four the other half of the next row: they
@@ -311,27 +342,31 @@ kv8_tiles_kernel(const Kv8Params p) {
             for (int pg = me; pg < kTilePages; pg += kTeam) {
                 const bool there = __shfl_sync(0xffffffffu, pages, pg) >= 0;
                 const uint32_t ratio = is_v ? __shfl_sync(0xffffffffu, ratios, pg) : 0u;
-                uint4 w[kUnits];
+#pragma unroll 1
+                for (int u0 = 0; u0 < kUnits; u0 += 2) {
+                    uint4 w[2];
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    w[u] = make_uint4(0, 0, 0, 0);
-                    if (there)
-                        w[u] = *reinterpret_cast<const uint4 *>(my_raw + pg * kBlock + u * 512 + urow * D + cc * 16);
-                }
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-                    uint32_t f[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) codes_to_f16<FMT>(in[k], f[2 * k], f[2 * k + 1]);
-                    if constexpr (is_v) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = mul_f16x2(f[k], ratio);
+                    for (int u = 0; u < 2; ++u) {
+                        w[u] = make_uint4(0, 0, 0, 0);
+                        if (there)
+                            w[u] = *reinterpret_cast<const uint4 *>(my_raw + pg * kBlock + (u0 + u) * 512 + urow * D + cc * 16);
                     }
-                    const int row = u * kUnitRows + urow;
-                    uint8_t *to = tile + pg * 2048;
-                    *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) codes_to_f16<FMT>(in[k], f[2 * k], f[2 * k + 1]);
+                        if constexpr (is_v) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = mul_f16x2(f[k], ratio);
+                        }
+                        // two units are 8 or 16 rows, so the swizzle goes by u alone
+                        uint8_t *to = tile + pg * 2048 + u0 * (kUnitRows * 128);
+                        const int row = u * kUnitRows + urow;
+                        *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4 *>(to + sw128_offset(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
                 }
             }
         };
@@ -357,17 +392,14 @@ kv8_tiles_kernel(const Kv8Params p) {
             return wait_for(&empty[j % kStages], ((j / kStages) & 1) ^ 1) && (!is_v || j != 1 || wait_for(&tree_read, 0));
         };
 
-        float vref = 0.f, vratio = 0.f;                      // both teams keep the same reference
+        float vref = 0.f;                                    // both teams keep the same reference
         auto take_scale = [&](float vs) {                    // largest scale of a tile
-            vratio = 1.f;
-            if (vs > 2.f * vref) {
-                vratio = vref / vs;
-                vref = vs;
-            }
+            if (vs > 2.f * vref) vref = vs;
         };
+        // page numbers two tiles ahead, scales one: neither is waited for
         int pages = load_pages(0), pages_next = load_pages(1);
-        float ks = 0.f, vs = 0.f;
-        auto load_scales = [&]() {
+        float ks, vs, ks_next, vs_next;
+        auto load_scales = [&](int pages, float &ks, float &vs) {
             ks = vs = 0.f;
             if (pages >= 0) {
                 const size_t block = (size_t)pages * a.Hkv + g;
@@ -376,32 +408,32 @@ kv8_tiles_kernel(const Kv8Params p) {
             }
         };
         fetch(pages);
-        load_scales();
+        load_scales(pages, ks, vs);
         bool ok = true;
         for (int j = 0; j < n_pre; ++j) {
+            load_scales(pages_next, ks_next, vs_next);
+            const int pages_after = load_pages(j + 2);
             // the tile's scales: the largest V scale decides the reference
             float top = fabsf(vs);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             take_scale(__shfl_sync(0xffffffffu, top, 0));
+            const float ratio = vref > 0.f ? vs / vref : 0.f;
+            ok = wait_for(landed, j & 1) && stage_free(j);
+            if (!ok) break;
             if (!is_v && me == 0) {
                 TileInfo &ti = info[j % kSlots];
                 if (lane < kTilePages)                       // a page past the prefix: its columns are masked
                     ti.ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
-                if (lane == 0) {
-                    ti.vref = vref;
-                    ti.vratio = vratio;
-                }
+                if (lane == 0) ti.vref = vref;
             }
-            const float ratio = vref > 0.f ? vs / vref : 0.f;
-            ok = wait_for(landed, j & 1) && stage_free(j);
-            if (!ok) break;
             store(tiles + (j % kStages) * L::kStage, pages, pack_f16(ratio, ratio));
             hand_over(&full[j % kStages]);
             pages = pages_next;
             fetch(pages);
-            load_scales();
-            pages_next = load_pages(j + 2);
+            pages_next = pages_after;
+            ks = ks_next;
+            vs = vs_next;
         }
         if (!ok) {                                           // copies in flight land before this warp leaves
             int zero = 0;
@@ -409,8 +441,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             mbar_wait(landed, 1, (volatile int *)&zero);
         }
         // bf16 tiles, copied asynchronously to their places, all of a tile's rows
-        // at once.  K is handed over after V, so that what is noted about V's rows
-        // is there when the scores are.
+        // at once.
         constexpr int kRow16 = D / 8;                        // 16-byte chunks of a bf16 row
         constexpr int kTailUnits = kTileKeys * kRow16 / 32;  // 512 bytes each
         constexpr int kTailRows = 32 / kRow16;
@@ -434,15 +465,14 @@ kv8_tiles_kernel(const Kv8Params p) {
             const int slot0 = tail_slot(j);
             TileInfo &ti = info[j % kSlots];
             take_scale(1.f);
+            ok = stage_free(j);
+            if (!ok) break;
             if (is_v) {
                 if (lane < kTileKeys / 32) ti.bad[me][lane] = 0;
                 __syncwarp();
             } else if (me == 0 && lane == 0) {
                 ti.vref = vref;
-                ti.vratio = vratio;
             }
-            ok = stage_free(j);
-            if (!ok) break;
             uint8_t *tile = sKV + (is_v ? L::kKV : 0) + (j % kStages) * L::kStage + (tc >> 3) * (kTileKeys * 128);
 #pragma unroll 2
             for (int u = me; u < kTailUnits; u += kTeam) {
@@ -474,9 +504,6 @@ kv8_tiles_kernel(const Kv8Params p) {
                         if (tc == 0) atomicOr(&ti.bad[me][row >> 5], 1u << (row & 31));
                     }
                 }
-            } else {
-                ok = wait_for(&v_full[j % kStages], (j / kStages) & 1);
-                if (!ok) break;
             }
             hand_over(&full[j % kStages]);
         }
@@ -491,50 +518,56 @@ kv8_tiles_kernel(const Kv8Params p) {
             convert(std::false_type{}, std::integral_constant<int, kKTeam>{}, warp - kMmaWarp - 1);
         } else if (lane == 0 && ntiles > 0) {
             const uint32_t aQ = smem_addr(sQ), aKV = smem_addr(sKV);
-            if (ngroups > 1)
-                kv8_mma_loop<D, 2>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full, o_done,
-                                   &q_ready, &drain_bar, &abort_sh, a.dev_status);
+            if (dual)
+                kv8_mma_loop<D, true>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full,
+                                      o_done, &q_ready, &drain_bar, &abort_sh, a.dev_status);
             else
-                kv8_mma_loop<D, 1>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full, o_done,
-                                   &q_ready, &drain_bar, &abort_sh, a.dev_status);
+                kv8_mma_loop<D, false>(tmem, aQ, aKV, ntiles, n_pre, k_full, v_full, k_empty, v_empty, s_full, p_full,
+                                       o_done, &q_ready, &drain_bar, &abort_sh, a.dev_status);
         }
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
         // ---------------------------------------------------------- softmax
         const int grp = (warp - kSoftmaxWarp0) >> 2, sub = warp & 3;
-        const int grow = sub * 32 + lane, row = grp * kGroupRows + grow;
+        const int grow = sub * 32 + lane;            // row within the group == TMEM lane
+        const int first_row = dual ? 0 : grp * kGroupRows, row = first_row + grow;
         const uint32_t lane_addr = (uint32_t)(sub * 32) << 16;
         const uint32_t tS = tmem + grp * 128 + lane_addr, tO = tmem + 256 + grp * D + lane_addr;
         const int gt = threadIdx.x - 32 * (kSoftmaxWarp0 + 4 * grp);       // 0..127 in the group
         const bool row_valid = row < rows_here;
         const int rg = m0 + row, node = rg / G, head = g * G + rg % G;
 
-        // The group's rows of Q into its operand region, bf16 or, scaled by a
+        // The group's tiles: every one, or every other from its own number on.
+        const int j0 = dual ? grp : 0, step = dual ? 2 : 1;
+
+        // The group's rows of Q into its operand region, as bf16 or, scaled by a
         // power of two that brings the row's largest magnitude to [2^13, 2^14),
-        // fp16.  D / 8 neighbouring threads share a row; all loads go out first.
+        // as fp16 in place.  D / 8 neighbouring threads share a row.
         constexpr int kRow16 = D / 8;
         constexpr int kQIters = kGroupRows * kRow16 / 128;
         const int qc = gt % kRow16;
         uint8_t *q_at = sQ + grp * L::kQGroup + (qc >> 3) * (kGroupRows * 128);
         {
-            const bool as_f16 = n_pre > 0;
             const float inv_g = 1.f / (float)G;              // (row + 1/2) / G truncates to the node
-            uint4 w[kQIters];
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < kQIters; ++i) {
-                const int rgg = m0 + grp * kGroupRows + i * (128 / kRow16) + gt / kRow16;
+                const int rr = i * (128 / kRow16) + gt / kRow16, rgg = m0 + first_row + rr;
                 const int nd = (int)(((float)rgg + 0.5f) * inv_g);
                 const size_t qi = ((size_t)(r.base + nd) * a.Hq + g * G + (rgg - nd * G)) * D + qc * 8;
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (rgg < rows_total && JSV_IN_BOUNDS(qi + 7, (long long)a.total_nodes * a.Hq * D, a.dev_status))
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + qi));
+                const bool in = rgg < rows_total && JSV_IN_BOUNDS(qi + 7, (long long)a.total_nodes * a.Hq * D, a.dev_status);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(q_at + sw128_offset(rr, qc & 7))),
+                             "l"(p.q + (in ? qi : 0)), "r"(in ? 16 : 0)
+                             : "memory");
             }
-#pragma unroll
-            for (int i = 0; i < kQIters; ++i) {
-                const int rr = i * (128 / kRow16) + gt / kRow16;
-                if (as_f16) {
-                    uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                          __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (j0 < n_pre) {
+#pragma unroll 4
+                for (int i = 0; i < kQIters; ++i) {
+                    const int rr = i * (128 / kRow16) + gt / kRow16;
+                    uint4 *at = reinterpret_cast<uint4 *>(q_at + sw128_offset(rr, qc & 7));
+                    const uint4 w = *at;
+                    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                          __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
                     m = max(m & 0xffffu, m >> 16);
 #pragma unroll
                     for (int off = 1; off < kRow16; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -544,9 +577,8 @@ kv8_tiles_kernel(const Kv8Params p) {
                     auto two = [&](uint32_t x) {
                         return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
                     };
-                    w[i] = make_uint4(two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
+                    *at = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
                 }
-                *reinterpret_cast<uint4 *>(q_at + sw128_offset(rr, qc & 7)) = w[i];
             }
             fence_async_smem();
         }
@@ -576,7 +608,7 @@ kv8_tiles_kernel(const Kv8Params p) {
         named_barrier(1, kGroups * 128);         // Q, row factors and parents are in place
         if (lane == 0) mbar_arrive(&q_ready);
         // kept normal, so that a masked score stays -inf under it
-        const float fac = fmaxf(p.scale_log2 * row_inv[row], 1.2e-38f);
+        const float fac = fmaxf(p.scale_log2 * row_inv[grp * kGroupRows + grow], 1.2e-38f);
         uint32_t anc[kTreeWords];                // this row's ancestors and itself (local memory: read in bf16 tiles only)
         if (has_tail && row_valid) {
             for (int w = 0; w < kTreeWords; ++w) anc[w] = 0;
@@ -597,88 +629,110 @@ kv8_tiles_kernel(const Kv8Params p) {
 
         float m_used = -INFINITY, l = 0.f, vref = 0.f;
         bool ok = true;
-        const int my_tiles = grp < ngroups ? ntiles : 0;
+        const int my_tiles = max(0, (ntiles - j0 + step - 1) / step);
+        int done = 0;                                // tiles of this group so far
         auto one_tile = [&](int j, auto tail_c) -> bool {
             constexpr bool is_tail = decltype(tail_c)::value;
-            if (!mbar_wait(&s_full[grp], j & 1, &abort_sh)) ok = false;
+            if (!mbar_wait(&s_full[grp], done & 1, &abort_sh)) ok = false;
+            // what is noted about the rows of a bf16 V tile comes with the tile
+            if (is_tail && !mbar_wait(&v_full[j % kStages], (j / kStages) & 1, &abort_sh)) ok = false;
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 return false;
             }
             tc_fence_after();
             const TileInfo &ti = info[j % kSlots];
-            // the whole row of 128 scores in registers: one TMEM round trip
-            uint32_t sv[kTileKeys / 32][32];
-#pragma unroll
-            for (int c = 0; c < kTileKeys / 32; ++c) tmem_ld_32x32b_x32(tS + c * 32, sv[c]);
-            // what brings each page's 16 columns to log2 units
-            float cs[kTilePages];
-            if constexpr (!is_tail) {
-                const float4 k0 = *reinterpret_cast<const float4 *>(&ti.ks[0]);
-                const float4 k1 = *reinterpret_cast<const float4 *>(&ti.ks[4]);
-                cs[0] = fac * k0.x, cs[1] = fac * k0.y, cs[2] = fac * k0.z, cs[3] = fac * k0.w;
-                cs[4] = fac * k1.x, cs[5] = fac * k1.y, cs[6] = fac * k1.z, cs[7] = fac * k1.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < kTilePages; ++k) cs[k] = p.scale_log2;
-            }
-            const float vratio = ti.vratio;
-            vref = ti.vref;
-            tmem_ld_wait();
+            // The row's 128 scores, 64 columns at a time.  The weights go over the
+            // first 64 columns, so the second half is read for the maximum,
+            // dropped, and read again for its weights.  The weights' loop is kept
+            // rolled: with the whole row unrolled, the softmax and the converting
+            // warps' code did not fit the instruction caches together.
+            uint32_t sv[2][32];
+            auto load_half = [&](int h) {
+                tmem_ld_32x32b_x32(tS + h * 64, sv[0]);
+                tmem_ld_32x32b_x32(tS + h * 64 + 32, sv[1]);
+            };
+            load_half(1);
+            // O is rescaled where the reference scale has changed since this group's last tile
+            const float vnew = ti.vref, vratio = vnew == vref ? 1.f : vref / vnew;
+            vref = vnew;
             // columns that are not seen become -inf: by a word of the tree's
             // visibility for 32 columns, or whole pages past the prefix in its last tile
+            uint32_t vis[kTileKeys / 32];
+            const int nb = is_tail ? kTilePages : pages8 - (t_begin + j) * kTilePages;       // pages this tile holds
             if constexpr (is_tail) {
                 const int slot0 = tail_slot(j);
 #pragma unroll
                 for (int c = 0; c < kTileKeys / 32; ++c) {
                     const int j0 = slot0 + c * 32 - r.P;         // tree node of column 32c (< 0: prefix, seen by all)
-                    uint32_t vis = 0u;
+                    vis[c] = 0u;
                     if (row_valid) {
                         if (j0 <= -32) {
-                            vis = 0xffffffffu;
+                            vis[c] = 0xffffffffu;
                         } else if (j0 < 0) {
-                            vis = (anc[0] << (-j0)) | ((1u << (-j0)) - 1u);
+                            vis[c] = (anc[0] << (-j0)) | ((1u << (-j0)) - 1u);
                         } else if (j0 < kMaxTreeNodes) {
                             const int w = j0 >> 5;
-                            vis = __funnelshift_r(anc[w], w + 1 < kTreeWords ? anc[w + 1] : 0u, j0 & 31);
+                            vis[c] = __funnelshift_r(anc[w], w + 1 < kTreeWords ? anc[w + 1] : 0u, j0 & 31);
                         }
-                        if (vis & (ti.bad[0][c] | ti.bad[1][c] | ti.bad[2][c] | ti.bad[3][c])) l = __uint_as_float(0x7fc00000u);
+                        if (vis[c] & (ti.bad[0][c] | ti.bad[1][c] | ti.bad[2][c] | ti.bad[3][c])) l = __uint_as_float(0x7fc00000u);
                     }
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) sv[c][x] = ((vis >> x) & 1u) ? sv[c][x] : 0xff800000u;
                 }
-            } else {
-                const int nb = pages8 - (t_begin + j) * kTilePages;        // pages this tile holds
-                if (nb < kTilePages) {
+            }
+            auto mask_half = [&](int h) {
+                if constexpr (is_tail) {
 #pragma unroll
-                    for (int c = 0; c < kTileKeys / 32; ++c)
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t v = h ? vis[2 + c] : vis[c];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) sv[c][x] = ((v >> x) & 1u) ? sv[c][x] : 0xff800000u;
+                    }
+                } else if (nb < kTilePages) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            if (2 * c + x / 16 >= nb) sv[c][x] = 0xff800000u;
+                            if (h * 4 + 2 * c + x / 16 >= nb) sv[c][x] = 0xff800000u;
                 }
-            }
+            };
+            // what brings each page's 16 columns to log2 units
+            auto factors = [&](int h) -> float4 {
+                if constexpr (is_tail) return make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                const float4 k = *reinterpret_cast<const float4 *>(&ti.ks[4 * h]);
+                return make_float4(fac * k.x, fac * k.y, fac * k.z, fac * k.w);
+            };
             // row maximum, a page at a time (scales are not negative)
             float tmax = -INFINITY;
+            auto max_half = [&](int h) {
+                const float4 f4 = factors(h);
+                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+                mask_half(h);
 #pragma unroll
-            for (int k = 0; k < kTilePages; ++k) {
-                const uint32_t *s = &sv[k / 2][(k & 1) * 16];
-                float u0 = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
-                float u1 = fmax3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t *s = &sv[k / 2][(k & 1) * 16];
+                    float u0 = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+                    float u1 = fmax3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
 #pragma unroll
-                for (int x = 6; x < 14; x += 4) {
-                    u0 = fmax3(u0, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-                    u1 = fmax3(u1, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+                    for (int x = 6; x < 14; x += 4) {
+                        u0 = fmax3(u0, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                        u1 = fmax3(u1, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+                    }
+                    u0 = fmax3(u0, __uint_as_float(s[14]), __uint_as_float(s[15]));
+                    tmax = fmaxf(tmax, fmaxf(u0, u1) * f[k]);
                 }
-                u0 = fmax3(u0, __uint_as_float(s[14]), __uint_as_float(s[15]));
-                tmax = fmaxf(tmax, fmaxf(u0, u1) * cs[k]);
-            }
+            };
+            tmem_ld_wait();
+            max_half(1);
+            load_half(0);
+            tmem_ld_wait();
+            max_half(0);
             float m_new = m_used;
             if (tmax > m_used + kMaxSlack) m_new = tmax;
             const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);     // 0 when m_used = -inf
             const float corr_o = corr * vratio;
             // O holds the earlier tiles' sum under the old maximum and reference
             // scale.  S_j was issued after PV_{j-1} and completes after it.
-            if (__any_sync(0xffffffffu, corr_o != 1.f) && j >= 1) {
+            if (__any_sync(0xffffffffu, corr_o != 1.f) && done > 0) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {
                     uint32_t ov[16];
@@ -695,15 +749,21 @@ kv8_tiles_kernel(const Kv8Params p) {
             uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             // bf16 values carry no scale of their own: their weights take 1 / vref
             const float unscale = is_tail ? 1.f / vref : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
+                if (h) {
+                    load_half(1);
+                    tmem_ld_wait();
+                    mask_half(1);
+                }
+                const float4 f4 = factors(h);
+                const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
                 uint32_t pk[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const int col = h * 64 + 2 * i;
-                    const float f = cs[col / 16];
-                    const uint64_t xa = f2_fma(f2_pack(__uint_as_float(sv[col / 32][col % 32]),
-                                                       __uint_as_float(sv[col / 32][col % 32 + 1])), f2_pack(f, f), base2);
+                    const float f = fs[i / 8];
+                    const uint64_t xa = f2_fma(f2_pack(__uint_as_float(sv[i / 16][2 * (i % 16)]),
+                                                       __uint_as_float(sv[i / 16][2 * (i % 16) + 1])), f2_pack(f, f), base2);
                     float u0, u1;
                     f2_unpack(xa, u0, u1);
                     u0 = fast_exp2(u0);
@@ -722,16 +782,16 @@ kv8_tiles_kernel(const Kv8Params p) {
             // the next tile is bf16, and so is Q from here on: this group's S of the
             // last 8-bit tile is complete, and the next is issued after these
             // warps' arrivals
-            if (!is_tail && has_tail && j + 1 == n_pre) q_to_bf16();
+            if (!is_tail && j + step >= n_pre && j + step < ntiles) q_to_bf16();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[grp]);
+            ++done;
             return true;
         };
-        for (int j = 0; j < min(n_pre, my_tiles); ++j)
-            if (!one_tile(j, std::false_type{})) break;
-        for (int j = n_pre; ok && j < my_tiles; ++j)
-            if (!one_tile(j, std::true_type{})) break;
+        int j = j0;
+        for (; ok && j < n_pre; j += step) one_tile(j, std::false_type{});
+        for (; ok && j < ntiles; j += step) one_tile(j, std::true_type{});
 
         bool have_o = ok && my_tiles > 0;
         if (have_o) {
@@ -746,6 +806,44 @@ kv8_tiles_kernel(const Kv8Params p) {
                 flag_error(a.dev_status, JSV_ERR_TIMEOUT);
             }
         }
+        // Where both groups have the same rows, the second hands its result to the
+        // first through the operand ring (every product has completed once both
+        // are at the barrier).
+        float4 *other = reinterpret_cast<float4 *>(sKV);             // [D / 4][128 rows]
+        float2 *other_ml = reinterpret_cast<float2 *>(sKV + kGroupRows * D * 4);
+        float mine = vref, theirs = 0.f;                             // factors of the two groups' O
+        if (dual) {
+            named_barrier(1, kGroups * 128);
+            if (grp == 1) {
+                other_ml[grow] = make_float2(m_used, l);
+                if (have_o) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t rr[16];
+                        tmem_ld_32x32b_x16(tO + c0, rr);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            other[(c0 / 4 + x) * kGroupRows + grow] =
+                                make_float4(__uint_as_float(rr[4 * x]) * vref, __uint_as_float(rr[4 * x + 1]) * vref,
+                                            __uint_as_float(rr[4 * x + 2]) * vref, __uint_as_float(rr[4 * x + 3]) * vref);
+                    }
+                }
+            }
+            named_barrier(1, kGroups * 128);
+            if (grp == 0) {
+                const float2 ml = other_ml[grow];
+                if (ntiles > 1 && !(ml.x == -INFINITY && ml.y == 0.f)) {
+                    const float M = fmaxf(m_used, ml.x);
+                    theirs = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+                    const float f = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_used - M);
+                    mine *= f;
+                    l = l * f + ml.y * theirs;
+                    m_used = M;
+                }
+            }
+        }
         // The rows, in whole rows through this warp's slice of the group's Q
         // region (every product of the group has completed), half of D at a time.
         const size_t rows = (size_t)a.total_nodes * a.Hq;
@@ -754,7 +852,9 @@ kv8_tiles_kernel(const Kv8Params p) {
         float4 *scr = reinterpret_cast<float4 *>(sQ + grp * L::kQGroup + sub * (32 * kScrCols * 4));
         if (have_o) tc_fence_after();
         auto write_rows = [&](long long my_off, float scale, auto store) {
-#pragma unroll
+            const bool add = __any_sync(0xffffffffu, theirs != 0.f);
+            const float s0 = mine * scale, s1 = theirs * scale;
+#pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
                 for (int c0 = 0; c0 < kScrCols; c0 += 32) {
@@ -767,10 +867,16 @@ kv8_tiles_kernel(const Kv8Params p) {
                         for (int x = 0; x < 32; ++x) rr[x] = 0u;
                     }
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        scr[lane * kChunks + ((c0 / 4 + x) ^ (lane & (kChunks - 1)))] =
-                            make_float4(__uint_as_float(rr[4 * x]) * scale, __uint_as_float(rr[4 * x + 1]) * scale,
-                                        __uint_as_float(rr[4 * x + 2]) * scale, __uint_as_float(rr[4 * x + 3]) * scale);
+                    for (int x = 0; x < 8; ++x) {
+                        float4 v = make_float4(__uint_as_float(rr[4 * x]) * s0, __uint_as_float(rr[4 * x + 1]) * s0,
+                                               __uint_as_float(rr[4 * x + 2]) * s0, __uint_as_float(rr[4 * x + 3]) * s0);
+                        if (add) {
+                            const float4 u = other[((pass * kScrCols + c0) / 4 + x) * kGroupRows + grow];
+                            v.x = fmaf(u.x, s1, v.x), v.y = fmaf(u.y, s1, v.y);
+                            v.z = fmaf(u.z, s1, v.z), v.w = fmaf(u.w, s1, v.w);
+                        }
+                        scr[lane * kChunks + ((c0 / 4 + x) ^ (lane & (kChunks - 1)))] = v;
+                    }
                 }
                 __syncwarp();
 #pragma unroll 4
@@ -783,15 +889,17 @@ kv8_tiles_kernel(const Kv8Params p) {
                 __syncwarp();
             }
         };
-        if (Sb == 1) {
-            write_rows(row_valid ? (long long)(row_id * D) : -1ll, l == 0.f ? 0.f : vref / l,
+        if (dual && grp == 1) {
+            // merged into the first group's rows
+        } else if (Sb == 1) {
+            write_rows(row_valid ? (long long)(row_id * D) : -1ll, l == 0.f ? 0.f : 1.f / l,
                        [&](long long o, const float4 &v) {
                            if (JSV_IN_BOUNDS(o + 3, (long long)rows * D, a.dev_status))
                                *reinterpret_cast<uint2 *>(p.out + o) = make_uint2(pack_bf16x2(v.x, v.y),
                                                                                   pack_bf16x2(v.z, v.w));
                        });
         } else {
-            write_rows(row_valid ? (long long)(((size_t)split * rows + row_id) * D) : -1ll, vref,
+            write_rows(row_valid ? (long long)(((size_t)split * rows + row_id) * D) : -1ll, 1.f,
                        [&](long long o, const float4 &v) {
                            if (JSV_IN_BOUNDS(o + 3, (long long)p.S * rows * D, a.dev_status))
                                *reinterpret_cast<float4 *>(p.ws_o + o) = v;
