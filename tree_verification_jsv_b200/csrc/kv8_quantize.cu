@@ -143,19 +143,26 @@ kv8_quantize_kernel(const QuantParams p) {
         m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
         const bool bad = m >= 0x7f80u;
         const float amax = __uint_as_float(m << 16);
-        // near the top of the range x * qmax would overflow: both sides of
-        // the quotient are taken 2^-32 times as large there (exact: what is
-        // lost at the bottom has code 0)
-        const float down = amax > 1.0e30f ? 2.3283064365386963e-10f : 1.f;
-        const float mul = down * kQmax, div = m ? amax * down : 1.f;
+        // at either end of the range both sides of the quotient are taken
+        // 2^-32 or 2^64 times as large, so that neither x * qmax nor 1 / amax
+        // overflows (exact, but for what has code 0)
+        const float size = amax > 1.0e30f ? 2.3283064365386963e-10f : amax < 1.0e-30f ? 1.8446744073709552e19f : 1.f;
+        const float mul = size * kQmax, div = m ? amax * size : 1.f, inv = 1.f / div;
+        // y / div from the reciprocal: the remainder of the first quotient is
+        // exact in one fma, and corrects it to 2^-24 and, where the quotient is
+        // a number of few bits (a tie between two codes), to that number
+        auto code = [&](float x) {
+            const float y = x * mul, q = y * inv;
+            return copysignf(fmaf(fmaf(-q, div, y), inv, q), x);       // the sum loses the sign of -0
+        };
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             float f[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                f[2 * j] = __uint_as_float(w[j] << 16) * mul / div;
-                f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * mul / div;
+                f[2 * j] = code(__uint_as_float(w[j] << 16));
+                f[2 * j + 1] = code(__uint_as_float(w[j] & 0xffff0000u));
             }
             uint2 c = make_uint2(code4<FMT>(f[0], f[1], f[2], f[3]), code4<FMT>(f[4], f[5], f[6], f[7]));
             if (bad) c = make_uint2(0, 0);

@@ -31,6 +31,7 @@ constexpr int kPoolCtas = 8;                 // one cluster (the portable size)
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 constexpr int kPageSlots = 16;
+constexpr int kRowBatch = 8;                 // row entries a lane reads at a time
 constexpr int kCounts = 64;                  // ints of exchanged counts at the workspace's start
 
 // Barrier over the cluster; the block's own barrier in front reconverges the
@@ -247,11 +248,20 @@ pages_fork_kernel(int num_pages, int32_t *__restrict__ refcount, int32_t *status
             const int a = src[i], d = dst[i], l = len[i];
             const int full = l / kPageSlots;
             part = !full_only && l % kPageSlots;
-            for (int e = lane; e < max_pages; e += 32) {
-                if (table[(size_t)d * max_pages + e] != -1) bad = 1;
-                if (e < full + part) {
-                    const int p = table[(size_t)a * max_pages + e];
-                    if (p == -1 ? e == full : (p < 0 || p >= num_pages || refcount[p] <= 0)) bad = 1;
+            // kRowBatch entries a lane at a time, so that their loads overlap
+            const int32_t *from = table + (size_t)a * max_pages, *to = table + (size_t)d * max_pages;
+            for (int e0 = lane; e0 < max_pages; e0 += 32 * kRowBatch) {
+                int p[kRowBatch];
+#pragma unroll
+                for (int k = 0; k < kRowBatch; ++k) {
+                    const int e = e0 + 32 * k;
+                    p[k] = e < full + part ? from[e] : -1;
+                    if (e < max_pages && to[e] != -1) bad = 1;
+                }
+#pragma unroll
+                for (int k = 0; k < kRowBatch; ++k) {
+                    if (p[k] == -1) bad |= part && e0 + 32 * k == full;
+                    else if (p[k] < 0 || p[k] >= num_pages || refcount[p[k]] <= 0) bad = 1;
                 }
             }
         }
@@ -288,11 +298,16 @@ pages_fork_kernel(int num_pages, int32_t *__restrict__ refcount, int32_t *status
         const int full = len[i] / kPageSlots;
         const int32_t *from = table + (size_t)src[i] * max_pages;
         int32_t *to = table + (size_t)dst[i] * max_pages;
-        for (int e = lane; e < full; e += 32) {
-            const int p = from[e];
-            if (p < 0) continue;
-            if (JSV_IN_BOUNDS(p, num_pages, status)) atomicAdd(&refcount[p], 1);
-            to[e] = p;
+        for (int e0 = lane; e0 < full; e0 += 32 * kRowBatch) {
+            int p[kRowBatch];
+#pragma unroll
+            for (int k = 0; k < kRowBatch; ++k) p[k] = e0 + 32 * k < full ? from[e0 + 32 * k] : -1;
+#pragma unroll
+            for (int k = 0; k < kRowBatch; ++k) {
+                if (p[k] < 0) continue;
+                if (JSV_IN_BOUNDS(p[k], num_pages, status)) atomicAdd(&refcount[p[k]], 1);
+                to[e0 + 32 * k] = p[k];
+            }
         }
         if (part && lane == 0 && JSV_IN_BOUNDS(prefix[i], num_pages, status)) {
             const int p = __ldcg(s.pages + prefix[i]);
