@@ -384,7 +384,8 @@ JSV_API jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 
  * and dev_status are used.  A request whose lengths are not
  * 0 <= from_len <= to_len or need a page past either table's row, or a page
  * whose entry is out of range, is flagged (JSV_ERR_DEVICE_INPUT) and skipped.
- * Two requests must not write the same 8-bit page in one call.
+ * Two requests must not write the same 8-bit page in one call; one that asks
+ * for more pages than the cache has is flagged and writes nothing.
  * Supported: B <= JSV_PAGES_MAX_ROWS.
  *   from_len, to_len   device [B] int32 (from_len may be NULL)
  */

@@ -52,14 +52,17 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
         return lo | (hi << 16);
     } else {
-        const uint32_t x = (uint32_t)__float2int_rn(a) & 255u, y = (uint32_t)__float2int_rn(b) & 255u;
-        const uint32_t z = (uint32_t)__float2int_rn(c) & 255u, w = (uint32_t)__float2int_rn(d) & 255u;
-        return x | (y << 8) | (z << 16) | (w << 24);
+        // 1.5 * 2^23 + x: the sum is rounded to a whole number, ties to even,
+        // whose low byte is the code
+        constexpr float kMagic = 12582912.f;
+        const uint32_t lo = __byte_perm(__float_as_uint(a + kMagic), __float_as_uint(b + kMagic), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(c + kMagic), __float_as_uint(d + kMagic), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
     }
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kQuantThreads)
+__global__ void __launch_bounds__(kQuantThreads, 4)
 kv8_quantize_kernel(const QuantParams p) {
     pdl_allow_dependents();
     pdl_wait_predecessor();
@@ -103,10 +106,14 @@ kv8_quantize_kernel(const QuantParams p) {
     const int row = lane / kLanesPerRow, col = lane % kLanesPerRow;
     // items in the order page, K or V, head: neighbouring warps read
     // neighbouring heads of one page
-    const long long items = (long long)pages * 2 * a.Hkv;
-    for (long long it = (long long)blockIdx.x * kQuantWarps + warp; it < items;
-         it += (long long)gridDim.x * kQuantWarps) {
-        const int g = (int)(it % a.Hkv), is_v = (int)(it / a.Hkv) & 1, pr = (int)(it / (2 * a.Hkv));
+    const long long all = (long long)pages * 2 * a.Hkv;
+    if (pages > p.c.num_pages && blockIdx.x == 0 && threadIdx.x == 0)      // some page is to be written twice
+        flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+    // num_pages * Hkv * 16 is below 2^31, so these stay far inside 32 bits
+    const unsigned items = pages > p.c.num_pages ? 0u : (unsigned)all, heads = (unsigned)a.Hkv;
+    for (unsigned it = blockIdx.x * kQuantWarps + warp; it < items; it += gridDim.x * kQuantWarps) {
+        const unsigned pk = it / heads;
+        const int g = (int)(it - pk * heads), is_v = (int)(pk & 1), pr = (int)(pk >> 1);
         int b = 0, top = a.B;                       // the last b with first[b] <= pr
         while (top - b > 1) {
             const int mid = (b + top) / 2;
@@ -153,7 +160,8 @@ kv8_quantize_kernel(const QuantParams p) {
         // a number of few bits (a tie between two codes), to that number
         auto code = [&](float x) {
             const float y = x * mul, q = y * inv;
-            return copysignf(fmaf(fmaf(-q, div, y), inv, q), x);       // the sum loses the sign of -0
+            const float exact = fmaf(fmaf(-q, div, y), inv, q);
+            return FMT == JSV_KV8_E4M3 ? copysignf(exact, x) : exact;      // the sum loses the sign of -0
         };
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
