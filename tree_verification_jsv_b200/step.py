@@ -209,3 +209,82 @@ class VerifyStep:
         once the current stream has been synchronised)."""
         self._host_graph.replay()
         return self._out.host
+
+
+class VerifyStepKv8(VerifyStep):
+    """The verify step over a prefix held in 8 bits, with its pages managed on
+    the device.
+
+    The full pages of every prefix are quantised once at the start and their
+    bf16 pages freed; ``run`` (and ``capture`` / ``replay``, ``run_host``) is
+    then the base class's step with ``jsv_tree_attention_kv8``.  ``advance``
+    follows a step: the pages that the accepted tokens filled are written to
+    the 8-bit cache, what the bf16 table no longer needs is freed, and pages
+    for the next tree are mapped, all on the stream, so that the caller only
+    writes the next tree's K/V and runs again.  A prefix may grow by as much as
+    the page table's row holds.
+    """
+
+    def __init__(self, wl, tokens, fmt="e4m3", device="cuda", max_path=None):
+        super().__init__(wl, tokens, device, max_path)
+        dev, B, width = self.device, self.B, wl.page_table.shape[1]
+        self.width = width
+        self.batch = jsv.make_batch(
+            B=B, Hq=self.Hq, Hkv=self.Hkv, D=self.D, max_pages_per_req=width, num_pages=wl.num_pages,
+            total_nodes=self.T, max_nodes=wl.max_nodes, max_prefix=width * 16 - 1, page_table=self.page_table,
+            prefix_len=self.prefix_len, node_offsets=self.node_offsets, parent=self.parent, dev_status=self.status)
+        pages8 = B * width
+        self.k8, self.v8 = (torch.zeros((pages8, self.Hkv, 16, self.D), dtype=torch.uint8, device=dev) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.zeros((pages8, self.Hkv), device=dev) for _ in range(2))
+        self.page_table8 = torch.full((B, width), -1, dtype=torch.int32, device=dev)
+        self.cache8 = jsv.make_kv8(format=fmt, num_pages=pages8, max_pages_per_req=width, k=self.k8, v=self.v8,
+                                   k_scale=self.k_scale, v_scale=self.v_scale, page_table=self.page_table8)
+        held = wl.page_table[wl.page_table >= 0]
+        self.refcount = _i32(np.bincount(held, minlength=wl.num_pages), dev)
+        self.refcount8 = torch.zeros(pages8, dtype=torch.int32, device=dev)
+        self.pool = jsv.make_page_pool(num_pages=wl.num_pages, refcount=self.refcount, dev_status=self.status)
+        self.pool8 = jsv.make_page_pool(num_pages=pages8, refcount=self.refcount8, dev_status=self.status)
+        self.nodes = self.node_offsets[1:] - self.node_offsets[:-1]
+        self.tree_end = torch.empty_like(self.prefix_len)
+        self.pages_ws = torch.empty(max(jsv.jsv_pages_workspace_size(n, B) for n in (wl.num_pages, pages8)),
+                                    dtype=torch.uint8, device=dev)
+        self.attn_ws = torch.empty(max(jsv.jsv_tree_attention_kv8_workspace_size(self.batch, self.cache8), 256),
+                                   dtype=torch.uint8, device=dev)
+        torch.add(self.prefix_len, self.nodes, out=self.tree_end)
+        self._write_full_pages(None, self.prefix_len, None)
+        jsv.jsv_pages_trim(self.pool, self.page_table, B, width, self.prefix_len, self.tree_end)
+
+    def _write_full_pages(self, from_len, to_len, stream):
+        jsv.jsv_pages_alloc(self.pool8, self.page_table8, self.B, self.width, None, to_len, True, self.pages_ws,
+                            stream=stream)
+        jsv.jsv_kv8_quantize(self.batch, self.cache8, self.k_cache, self.v_cache, from_len, to_len, stream=stream)
+
+    def attention(self, stream=None):
+        jsv.jsv_tree_attention_kv8(self.batch, self.cache8, self.q, self.k_cache, self.v_cache, self.scale, self.out,
+                                   self.attn_ws, stream=stream)
+
+    def advance(self, stream=None):
+        """The turn to the next step: ``prefix_len`` becomes ``new_len``.
+        ``stream``: a torch stream, the one the step ran on, or None for the
+        current one."""
+        with torch.cuda.stream(stream):
+            self._write_full_pages(self.prefix_len, self.new_len, stream)
+            jsv.jsv_pages_trim(self.pool, self.page_table, self.B, self.width, self.new_len, self.new_len,
+                               stream=stream)
+            self.prefix_len.copy_(self.new_len)
+            torch.add(self.new_len, self.nodes, out=self.tree_end)
+            jsv.jsv_pages_alloc(self.pool, self.page_table, self.B, self.width, self.new_len, self.tree_end, False,
+                                self.pages_ws, stream=stream)
+
+    def run_host(self, stream=None):
+        """As the base class's, but for the page table and the prefix lengths,
+        which live on the device: of the pinned inputs, what follows them is
+        copied up."""
+        at = self._in.layout["node_offsets"][0]
+        self._in.dev_buf[at:].copy_(self._in.host_buf[at:], non_blocking=True)
+        self.run(stream)
+        self._out.host_buf.copy_(self._out.dev_buf, non_blocking=True)
+        return self._out.host
+
+    def h2d_bytes(self) -> int:
+        return self._in.nbytes - self._in.layout["node_offsets"][0]
