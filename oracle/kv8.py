@@ -93,12 +93,15 @@ def tree_attention(case, fmt):
             codes[s0:s0 + n, g * G:(g + 1) * G] = np.abs(decode(case["v8"][pg8, g], fmt)).sum(axis=(0, 1)) * \
                 case["v_scale"][pg8, g].max(initial=0)
             for h in range(g * G, (g + 1) * G):
-                for i in range(n):
-                    at = np.flatnonzero(sees[i])
-                    s = case["scale"] * (K[at] @ q[s0 + i, h])
-                    p = np.exp(s - s.max())
-                    p /= p.sum()
-                    out[s0 + i, h] = p @ V[at]
-                    mag[s0 + i, h] = p @ np.abs(V[at])
-                    top[s0 + i, h] = case["scale"] * (np.abs(K[at]) @ np.abs(q[s0 + i, h])).max()
+                qh = q[s0:s0 + n, h]
+                with np.errstate(invalid="ignore"):
+                    s = np.where(sees, case["scale"] * (qh @ K.T), -np.inf)
+                    p = np.exp(s - s.max(axis=1, keepdims=True))
+                    p /= p.sum(axis=1, keepdims=True)
+                    # a key that a node does not see has weight zero whatever its value is
+                    odd = ~np.isfinite(V)
+                    V0 = np.where(odd, 0, V)
+                    out[s0:s0 + n, h], mag[s0:s0 + n, h] = p @ V0, p @ np.abs(V0)
+                    out[s0:s0 + n, h][(sees.astype(np.int64) @ odd) > 0] = np.nan
+                    top[s0:s0 + n, h] = case["scale"] * np.where(sees, np.abs(qh) @ np.abs(K).T, 0).max(axis=1)
     return out, mag, top, codes

@@ -79,7 +79,7 @@ struct RowSmem {
     static constexpr int kWarp = kRing > kMerge ? kRing : kMerge;
     static constexpr int kTotal = kRowWarps * kWarp + 1024;
     // CTAs an SM that the registers are to leave room for
-    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+    static constexpr int kCtas = NT == 1 ? 4 : 3;
 };
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
@@ -128,15 +128,18 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int e8 = min(t1, pages8), f8 = t0 + warp;
     const int count = e8 > f8 ? (e8 - f8 + kRowWarps - 1) / kRowWarps : 0;
     const int oob = (int)((long long)p.c.num_pages * a.Hkv * 16);          // a row past the codes: reads zeros
-    // lane l holds the row coordinate and scales of the warp's page 32 grp + l
-    auto load_group = [&](int grp, int &row, float &ks, float &vs) {
+    // lane l holds the row coordinate and scales of the warp's page 32 grp + l;
+    // `page` is the table's entry, looked up beforehand
+    auto look_up = [&](int grp) -> int {
         const int i = grp * 32 + lane;
+        const long long pi = (long long)b * p.c.max_pages_per_req + f8 + i * kRowWarps;
+        return i < count && JSV_IN_BOUNDS(pi, (long long)a.B * p.c.max_pages_per_req, a.dev_status)
+                   ? __ldg(p.c.page_table + pi) : -1;
+    };
+    auto load_group = [&](int grp, int page, int &row, float &ks, float &vs) {
         row = oob;
         ks = vs = 0.f;
-        if (i < count) {
-            const long long pi = (long long)b * p.c.max_pages_per_req + f8 + i * kRowWarps;
-            int page = -1;
-            if (JSV_IN_BOUNDS(pi, (long long)a.B * p.c.max_pages_per_req, a.dev_status)) page = __ldg(p.c.page_table + pi);
+        if (grp * 32 + lane < count) {
             if (page >= 0 && page < p.c.num_pages) {
                 const size_t block = (size_t)page * a.Hkv + g;
                 row = (int)block * 16;
@@ -147,47 +150,27 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
         }
     };
-    int row_c, row_n;
-    float ks_c, vs_c, ks_n, vs_n;
-    load_group(0, row_c, ks_c, vs_c);
-    load_group(1, row_n, ks_n, vs_n);
-    auto issue = [&](int i, int group) {             // page i of the warp, `group` the one in row_c
-        const int row = __shfl_sync(0xffffffffu, (i >> 5) == group ? row_c : row_n, i & 31);
-        if (lane == 0) {
-            const int s = i % kRowStages;
-            uint8_t *dst = ring + s * 2 * L::kBlock;
-            mbar_arrive_expect_tx(&full[warp][s], 2 * L::kBlock);
-            tma_load_2d(dst, &tmK, &full[warp][s], 0, row);
-            tma_load_2d(dst + L::kBlock, &tmV, &full[warp][s], 0, row);
-        }
-    };
-    for (int i = 0; i < min(count, kRowStages); ++i) issue(i, 0);
-
-    // ancestors of the rows, where this CTA holds any of the tree's pages
+    // What depends on nothing but the request goes out together, before the
+    // first wait for any of it: page numbers, Q, parents, the first bf16 page.
     const bool has_tail = t1 > pages8;
-    if (has_tail) {
-        for (int i = threadIdx.x; i < r.n; i += kRowWarps * 32)
-            par_sh[i] = JSV_IN_BOUNDS(r.base + i, a.total_nodes, a.dev_status) ? __ldg(a.parent + r.base + i) : -1;
-        __syncthreads();
-        if (threadIdx.x < kRows) {
-            const int row = threadIdx.x, rg = m0 + row;
-            for (int w = 0; w < kTreeWords; ++w) anc[row][w] = 0;
-            if (rg < rows_total) {
-                int j = rg / G;
-                while (j != -1) {
-                    anc[row][j >> 5] |= 1u << (j & 31);
-                    const int pj = par_sh[j];
-                    if (j == 0 ? pj != -1 : (pj < 0 || pj >= j)) {
-                        flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
-                        break;
-                    }
-                    j = pj;
-                }
-            }
-        }
-        __syncthreads();
+    const int first_tail = max(t0, pages8);
+    const int tail0 = first_tail + ((warp - (first_tail - t0)) % kRowWarps + kRowWarps) % kRowWarps;
+    auto tail_page = [&](int lp) -> int {
+        const long long pi = (long long)b * a.max_pages_per_req + lp;
+        return lp < t1 && JSV_IN_BOUNDS(pi, (long long)a.B * a.max_pages_per_req, a.dev_status)
+                   ? __ldg(a.page_table + pi) : -1;
+    };
+    const int page_c = look_up(0);
+    int page_n = look_up(1);
+    int tail_next = has_tail ? tail_page(tail0) : -1;
+    constexpr int kParents = kMaxTreeNodes / (kRowWarps * 32);
+    int par[kParents];
+#pragma unroll
+    for (int k = 0; k < kParents; ++k) {
+        const int i = threadIdx.x + k * (kRowWarps * 32);
+        par[k] = has_tail && i < r.n && JSV_IN_BOUNDS(r.base + i, a.total_nodes, a.dev_status)
+                     ? __ldg(a.parent + r.base + i) : -1;
     }
-
     // Q row n of each row tile, dims t*D/4 .., as bf16 pairs: words 2s, 2s+1
     // are k-step s.  Rows past the request are zero.
     uint32_t qb[NT][kSteps][2];
@@ -209,8 +192,50 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
         }
     };
-    float fac[NT][2];                            // rows 2t, 2t + 1: score to log2 units, before the K scale
     load_q();
+
+    int row_c, row_n;
+    float ks_c, vs_c, ks_n, vs_n;
+    load_group(0, page_c, row_c, ks_c, vs_c);
+    load_group(1, page_n, row_n, ks_n, vs_n);
+    page_n = look_up(2);
+    auto issue = [&](int i, int group) {             // page i of the warp, `group` the one in row_c
+        const int row = __shfl_sync(0xffffffffu, (i >> 5) == group ? row_c : row_n, i & 31);
+        if (lane == 0) {
+            const int s = i % kRowStages;
+            uint8_t *dst = ring + s * 2 * L::kBlock;
+            mbar_arrive_expect_tx(&full[warp][s], 2 * L::kBlock);
+            tma_load_2d(dst, &tmK, &full[warp][s], 0, row);
+            tma_load_2d(dst + L::kBlock, &tmV, &full[warp][s], 0, row);
+        }
+    };
+    for (int i = 0; i < min(count, kRowStages); ++i) issue(i, 0);
+
+    // ancestors of the rows, where this CTA holds any of the tree's pages
+    if (has_tail) {
+#pragma unroll
+        for (int k = 0; k < kParents; ++k) par_sh[threadIdx.x + k * (kRowWarps * 32)] = par[k];
+        __syncthreads();
+        if (threadIdx.x < kRows) {
+            const int row = threadIdx.x, rg = m0 + row;
+            for (int w = 0; w < kTreeWords; ++w) anc[row][w] = 0;
+            if (rg < rows_total) {
+                int j = rg / G;
+                while (j != -1) {
+                    anc[row][j >> 5] |= 1u << (j & 31);
+                    const int pj = par_sh[j];
+                    if (j == 0 ? pj != -1 : (pj < 0 || pj >= j)) {
+                        flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
+                        break;
+                    }
+                    j = pj;
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    float fac[NT][2];                            // rows 2t, 2t + 1: score to log2 units, before the K scale
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         // the row's largest magnitude to [2^13, 2^14)
@@ -308,7 +333,8 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             row_c = row_n;
             ks_c = ks_n;
             vs_c = vs_n;
-            load_group(grp + 1, row_n, ks_n, vs_n);
+            load_group(grp + 1, page_n, row_n, ks_n, vs_n);
+            page_n = look_up(grp + 2);
         }
         const float ks = __shfl_sync(0xffffffffu, ks_c, i & 31), vs = __shfl_sync(0xffffffffu, vs_c, i & 31);
         const int st = i % kRowStages;
@@ -391,14 +417,11 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 
     // The bf16 pages: the rest of the prefix (seen by all) and the tree's
     // slots (seen by their descendants and themselves), on bf16 operands.
-    const int first_tail = max(t0, pages8);
     if (ok && has_tail) {
         load_q();
-        for (int lp = first_tail + ((warp - (first_tail - t0)) % kRowWarps + kRowWarps) % kRowWarps; lp < t1;
-             lp += kRowWarps) {
-            const long long pi = (long long)b * a.max_pages_per_req + lp;
-            const int page = JSV_IN_BOUNDS(pi, (long long)a.B * a.max_pages_per_req, a.dev_status)
-                                 ? __ldg(a.page_table + pi) : -1;
+        for (int lp = tail0; lp < t1; lp += kRowWarps) {
+            const int page = tail_next;
+            tail_next = tail_page(lp + kRowWarps);
             if (page < 0 || page >= a.num_pages) {
                 if (lane == 0) flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
                 continue;
@@ -627,9 +650,21 @@ kv8_merge_kernel(const Kv8Params p) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// Query rows of a KV head (nodes * Hq / Hkv) up to which the page-streaming
-// form is taken.
-constexpr int kRowsFormMost = 32;
+// The page-streaming form costs by (page, KV head, 8 rows), the tcgen05 form by
+// (tile, KV head, 256 rows) and a fixed 15 us or so.  Up to 32 rows of a KV
+// head the first is taken whatever the length (32 heads over 8 KV heads, us,
+// streaming against tcgen05: 8 nodes over 32768 tokens 41 / 51, 16 requests of
+// 8 nodes over 4096 71 / 85), above that while there are few such units (16
+// nodes over 2048, 8,300 units: 17 / 21; 12 over 8192, 25,000: 25 / 29; 4 x 32
+// over 1024, 34,000: 27 / 24; 32 over 8192, 66,000: 39 / 31).
+constexpr int kStreamRows = 32;
+constexpr double kStreamUnits = 28000.0;
+// A warp takes 16 rows of a page together once there are enough units to go
+// round (16 requests of 4 nodes over 4096 tokens, 66,000 units: 42 us against 50
+// with 8 rows), 8 otherwise: twice the warps, and half the code to fetch, which
+// is what a short call waits for (16 nodes over 128 tokens 6.9 us against 7.3;
+// 12 over 2048, 6,200 units: 15 against 19).
+constexpr double kWideUnits = 16000.0;
 
 struct Kv8Plan {
     int nt;                                      // 8-row tiles of a warp, 0: the tcgen05 form
@@ -661,13 +696,14 @@ Kv8Plan plan_of(const BatchArgs &a, const jsv_kv8 &c) {
     const int rows = a.max_nodes * (a.Hq / a.Hkv);
     const int sms = std::max(device_sm_count(), 1);
     const double load = std::min(1.0, ((double)c.num_pages + a.B) / ((double)a.B * (a.max_prefix / 16 + 1)));
-    if (rows <= kRowsFormMost) {
-        pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    const double units = load * a.B * a.Hkv * ((a.max_prefix + (double)a.max_nodes + 15) / 16) * ((rows + 7) / 8);
+    if (rows <= kStreamRows || units <= kStreamUnits) {
+        pl.nt = rows <= 8 || units <= kWideUnits ? 1 : 2;
         const int tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
         const int total = (int)(((long long)a.max_prefix + a.max_nodes + 15) / 16);
-        // a warp takes about 0.4 us (8 rows) to 0.9 us (32) for a page
+        // a warp takes about 0.4 us (8 rows) to 0.6 us (16) for a page
         choose_splits(pl, (long long)a.B * a.Hkv * tiles, load, total, std::max(total / kRowWarps, 1),
-                      sms * (pl.nt == 1 ? 4 : pl.nt == 2 ? 3 : 2), kRowWarps, 8.0, 4.0, 0.05);
+                      sms * (pl.nt == 1 ? 4 : 3), kRowWarps, 8.0, 4.0, 0.05);
     } else {
         pl.nt = 0;
         const int tiles = (rows + 255) / 256;
@@ -708,7 +744,7 @@ cudaError_t launch_rows(const Kv8Params &p, cudaStream_t st) {
 
 template <int D, int FMT>
 cudaError_t launch_rows(const Kv8Params &p, int nt, cudaStream_t st) {
-    return nt == 1 ? launch_rows<D, FMT, 1>(p, st) : nt == 2 ? launch_rows<D, FMT, 2>(p, st) : launch_rows<D, FMT, 4>(p, st);
+    return nt == 1 ? launch_rows<D, FMT, 1>(p, st) : launch_rows<D, FMT, 2>(p, st);
 }
 
 template <int D>
