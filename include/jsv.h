@@ -18,7 +18,9 @@
  *   jsv_kv_compact      move the accepted path's K/V rows to contiguous
  *                       slots P..P+a of each request (ragged batches)
  *
- * jsv_accept_compact does the last two in one launch.
+ * jsv_accept_compact does the last two in one launch.  Over a prefix held in
+ * 8 bits jsv_tree_attention_kv8 takes the first call's place; the page pool's
+ * calls (jsv_pages_*) and jsv_kv8_quantize turn the pages over between steps.
  *
  * Conventions for every call
  *   - Pointers marked "device" are CUDA device (or managed) memory; the
@@ -316,7 +318,8 @@ JSV_API jsv_status jsv_lmhead_argmax_noalloc(const uint16_t *hidden, const uint1
  *     slots [16 * floor(P_b / 16), P_b + N_b)  bf16 pages, jsv_batch.page_table
  * Both tables are indexed by logical page (slot / 16); jsv_batch.page_table
  * entries below floor(P_b / 16) are not read, so their bf16 pages may be
- * freed or shared out again.  A value is code * scale.
+ * freed or shared out again.  A value is code * scale; scales are not
+ * negative.
  * Layout: codes [num_pages][Hkv][16][D] (the 16 x D block of one page and
  * head is contiguous), scales [num_pages][Hkv].
  * The pages that the README's engine keeps are bf16; this is a deployment
