@@ -16,7 +16,7 @@
 // latency: two or three rounds of dependent loads and as many barriers (alloc
 // 8-9 us, fork 12 us, compact 11-13 us under ncu on pools of 300 to 20,000
 // pages; rows' entries are read eight to a lane at a time, which took a fork of
-// 64 rows from 30 us to 17).  Trimming (4 us) and copying need no order between
+// 64 rows from 30 us to 20).  Trimming (4 us) and copying need no order between
 // CTAs and use plain grids.
 #include "jsv_internal.cuh"
 #include "kv_internal.cuh"

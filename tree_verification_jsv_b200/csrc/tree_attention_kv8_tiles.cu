@@ -77,7 +77,7 @@ constexpr float kWeightLog2 = 6.f;               // weights are held as 2^6 e: e
 // last tile has been read.
 struct __align__(16) TileInfo {
     float ks[kTilePages];                        // read as two float4
-    float vref;                                  // reference scale of V
+    float vref, vinv;                            // reference scale of V and its reciprocal
     // bf16 slots whose V row is not finite, as each converting warp found them
     uint32_t bad[kVTeam][kTileKeys / 32];
 };
@@ -403,9 +403,15 @@ kv8_tiles_kernel(const Kv8Params p) {
             return wait_for(&empty[j % kStages], ((j / kStages) & 1) ^ 1) && (!is_v || j != 1 || wait_for(&tree_read, 0));
         };
 
-        float vref = 0.f;                                    // both teams keep the same reference
+        // Both teams keep the same reference.  Its reciprocal stays finite: values
+        // of a scale below 1e-37 count as zero.  (A division here or in the
+        // softmax, with the code of its rare cases, cost 2%.)
+        float vref = 0.f, vinv = 0.f;
         auto take_scale = [&](float vs) {                    // largest scale of a tile
-            if (vs > 2.f * vref) vref = vs;
+            if (vs > 2.f * vref && vs > 1.0e-37f) {
+                vref = vs;
+                vinv = 1.f / vs;
+            }
         };
         // page numbers two tiles ahead, scales one: neither is waited for
         int pages = load_pages(0), pages_next = load_pages(1);
@@ -429,14 +435,17 @@ kv8_tiles_kernel(const Kv8Params p) {
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             take_scale(__shfl_sync(0xffffffffu, top, 0));
-            const float ratio = vref > 0.f ? vs / vref : 0.f;
+            const float ratio = vs * vinv;
             ok = wait_for(landed, j & 1) && stage_free(j);
             if (!ok) break;
             if (!is_v && me == 0) {
                 TileInfo &ti = info[j % kSlots];
                 if (lane < kTilePages)                       // a page past the prefix: its columns are masked
                     ti.ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
-                if (lane == 0) ti.vref = vref;
+                if (lane == 0) {
+                    ti.vref = vref;
+                    ti.vinv = vinv;
+                }
             }
             store(tiles + (j % kStages) * L::kStage, pages, pack_f16(ratio, ratio));
             hand_over(&full[j % kStages]);
@@ -483,6 +492,7 @@ kv8_tiles_kernel(const Kv8Params p) {
                 __syncwarp();
             } else if (me == 0 && lane == 0) {
                 ti.vref = vref;
+                ti.vinv = vinv;
             }
             uint8_t *tile = sKV + (is_v ? L::kKV : 0) + (j % kStages) * L::kStage + (tc >> 3) * (kTileKeys * 128);
 #pragma unroll 2
@@ -665,7 +675,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             };
             load_half(1);
             // O is rescaled where the reference scale has changed since this group's last tile
-            const float vnew = ti.vref, vratio = vnew == vref ? 1.f : vref / vnew;
+            const float vnew = ti.vref, vinv = ti.vinv, vratio = vnew == vref ? 1.f : vref * vinv;
             vref = vnew;
             // columns that are not seen become -inf: by a word of the tree's
             // visibility for 32 columns, or whole pages past the prefix in its last tile
@@ -759,7 +769,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             const uint64_t base2 = f2_pack(base, base);
             uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             // bf16 values carry no scale of their own: their weights take 1 / vref
-            const float unscale = is_tail ? 1.f / vref : 1.f;
+            const float unscale = is_tail ? vinv : 1.f;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (h) {
