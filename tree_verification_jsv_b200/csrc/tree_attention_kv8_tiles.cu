@@ -652,8 +652,11 @@ kv8_tiles_kernel(const Kv8Params p) {
         bool ok = true;
         const int my_tiles = max(0, (ntiles - j0 + step - 1) / step);
         int done = 0;                                // tiles of this group so far
-        auto one_tile = [&](int j, auto tail_c) -> bool {
-            constexpr bool is_tail = decltype(tail_c)::value;
+        // Three kinds of tile, each with code of its own, so that the many of the
+        // first kind run through little of it: 8-bit tiles; the group's last of
+        // them, which may hold fewer pages and is followed by bf16 tiles; those.
+        auto one_tile = [&](int j, auto kind_c) -> bool {
+            constexpr bool is_last = decltype(kind_c)::value == 1, is_tail = decltype(kind_c)::value == 2;
             if (!mbar_wait(&s_full[grp], done & 1, &abort_sh)) ok = false;
             // what is noted about the rows of a bf16 V tile comes with the tile
             if (is_tail && !mbar_wait(&v_full[j % kStages], (j / kStages) & 1, &abort_sh)) ok = false;
@@ -708,7 +711,7 @@ kv8_tiles_kernel(const Kv8Params p) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) sv[c][x] = ((v >> x) & 1u) ? sv[c][x] : 0xff800000u;
                     }
-                } else if (nb < kTilePages) {
+                } else if (is_last && nb < kTilePages) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -803,7 +806,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             // the next tile is bf16, and so is Q from here on: this group's S of the
             // last 8-bit tile is complete, and the next is issued after these
             // warps' arrivals
-            if (!is_tail && j + step >= n_pre && j + step < ntiles) q_to_bf16();
+            if (is_last && j + step < ntiles) q_to_bf16();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[grp]);
@@ -811,8 +814,12 @@ kv8_tiles_kernel(const Kv8Params p) {
             return true;
         };
         int j = j0;
-        for (; ok && j < n_pre; j += step) one_tile(j, std::false_type{});
-        for (; ok && j < ntiles; j += step) one_tile(j, std::true_type{});
+        for (; ok && j + step < n_pre; j += step) one_tile(j, std::integral_constant<int, 0>{});
+        if (ok && j < n_pre) {
+            one_tile(j, std::integral_constant<int, 1>{});
+            j += step;
+        }
+        for (; ok && j < ntiles; j += step) one_tile(j, std::integral_constant<int, 2>{});
 
         bool have_o = ok && my_tiles > 0;
         if (have_o) {
