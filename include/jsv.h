@@ -319,7 +319,7 @@ JSV_API jsv_status jsv_lmhead_argmax_noalloc(const uint16_t *hidden, const uint1
  * Both tables are indexed by logical page (slot / 16); jsv_batch.page_table
  * entries below floor(P_b / 16) are not read, so their bf16 pages may be
  * freed or shared out again.  A value is code * scale; scales are not
- * negative.
+ * negative, and V scales below 1e-37 may count as zero.
  * Layout: codes [num_pages][Hkv][16][D] (the 16 x D block of one page and
  * head is contiguous), scales [num_pages][Hkv].
  * The pages that the README's engine keeps are bf16; this is a deployment

@@ -32,16 +32,17 @@
 // when a page's scale passes 2 vref, and then O is rescaled with the running
 // maximum's correction.
 //
-// A tile takes about 4,300 cycles (timeline of one CTA, 256 nodes over 16384
-// tokens): softmax about 2,400 (scores from TMEM 230, maximum 450, exponentials,
-// packing and the store 1,600), then 1,400 until the group's PV and next S are
-// issued and complete, and 500 waiting for the thread that issues them.  The
-// tensor pipe's share is 2,048; tree_attention.cu, whose operands need no
-// conversion, takes 3,600.  What the converting warps execute slows the rest
-// through the instruction caches: code unrolled there costs more than it saves.
-// 256 nodes over 16384 tokens (int8) take 118 us (581 TFLOP/s, 35% of the
-// measured bf16 rate), four 512-node trees over 32768 1,387 us (793), a ragged
-// batch of 16 231 us.
+// A tile took about 4,300 cycles when 256 nodes over 16384 tokens took 118 us
+// (timeline of one CTA): softmax about 2,400 (scores from TMEM 230, maximum 450,
+// exponentials, packing and the store 1,600), then 1,400 until the group's PV
+// and next S are issued and complete, and 500 waiting for the thread that issues
+// them.  The tensor pipe's share is 2,048; tree_attention.cu, whose operands
+// need no conversion, takes 3,600.  All warps' code of a tile competes for the
+// instruction caches, so what runs rarely is kept out of the loops: a division's
+// rare cases cost 6%, the last tile's mask 3-4%, unrolled conversion 13%.
+// 256 nodes over 16384 tokens (int8) take 109 us (631 TFLOP/s, 38% of the
+// measured bf16 rate), four 512-node trees over 32768 1,264-1,316 us (835-870,
+// by the box's clock), a ragged batch of 16 210 us.
 #include "kv8_attention.cuh"
 
 #include <string.h>
@@ -405,7 +406,7 @@ kv8_tiles_kernel(const Kv8Params p) {
 
         // Both teams keep the same reference.  Its reciprocal stays finite: values
         // of a scale below 1e-37 count as zero.  (A division here or in the
-        // softmax, with the code of its rare cases, cost 2%.)
+        // softmax, with the code of its rare cases, cost 6%.)
         float vref = 0.f, vinv = 0.f;
         auto take_scale = [&](float vs) {                    // largest scale of a tile
             if (vs > 2.f * vref && vs > 1.0e-37f) {
