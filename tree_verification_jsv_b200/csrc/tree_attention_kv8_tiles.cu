@@ -8,15 +8,15 @@
 // CTA has 128 rows or fewer, both groups take the same rows and every other
 // tile each, and their results are merged at the end: one group alone would
 // leave the tensor core idle during its softmax (16 requests of 16 nodes over
-// 4096 tokens: 88 us with one group).  Also different is where the operands
-// come from: the codes are read by ordinary
-// 16-byte loads and written to the operand tiles as fp16 by seven converting
-// warps, one 128-key tile ahead, so the tensor core, the softmax and the
-// conversion run side by side.
+// 4096 tokens: 88 us with one group, 83 with two, which the conversion bounds).
+// Also different is where the operands come from: the codes are copied a page
+// at a time to shared memory and written from there to the operand tiles as
+// fp16 by seven converting warps, one 128-key tile ahead, so that the tensor
+// core, the softmax and the conversion run side by side.
 //
 // Tiles: eight 8-bit pages each (128 keys), then 128-slot tiles of the bf16
 // cache from the first slot past the full pages, copied unconverted and
-// multiplied as bf16: a group's warps put their rows of Q back as bf16 when
+// multiplied as bf16: a group's warps turn their rows of Q back to bf16 when
 // they hand over the last 8-bit tile's weights.
 //
 //   warps 0..3    V tiles: codes -> fp16, or bf16 copied
@@ -44,8 +44,6 @@
 // measured bf16 rate), four 512-node trees over 32768 1,264-1,316 us (835-870,
 // by the box's clock), a ragged batch of 16 210 us.
 #include "kv8_attention.cuh"
-
-#include <string.h>
 
 #include <type_traits>
 
