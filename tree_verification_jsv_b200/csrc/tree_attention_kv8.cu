@@ -70,7 +70,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 //                   neighbouring dims of rows 2t and 2t + 1
 //
 // Bound by instruction issue and latency more than by HBM: a page costs a warp
-// about 300 instructions (the codes' conversion is half of them), and a call
+// about 400 instructions with int8 codes (their conversion is half), and a call
 // about 12 us beside the pages (a chain of dependent loads, the merges, the
 // second launch).  One token of 16 requests over 512 to 8192 tokens (int8, 154
 // MB) takes 36 us, 4.2 TB/s, 65% of the measured copy rate; over 4096 tokens
