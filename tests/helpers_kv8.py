@@ -113,3 +113,31 @@ def assert_attention(got, case, fmt, what="", rows=None):
     if rows is not None:
         bad = bad[rows]
     assert not bad.any(), f"{what}: {bad.sum()} elements off, worst {np.nanmax(err / tol):.2f} of the bound"
+
+
+def aim(case, fmt, b, page, slot, strength):
+    """Every query of request b points at one key of its KV head's 8-bit
+    prefix; with keys of about unit normal values the key's score is
+    ``strength`` and the others' within about 0.6 of that."""
+    s0, s1 = case["node_offsets"][b], case["node_offsets"][b + 1]
+    q, G = synth.bf16_bits_to_f32(case["q"]).copy(), case["Hq"] // case["Hkv"]
+    for g in range(case["Hkv"]):
+        pg = case["page_table8"][b, page]
+        k = kv8.decode(case["k8"][pg, g, slot], fmt) * case["k_scale"][pg, g]
+        q[s0:s1, g * G:(g + 1) * G] = strength / case["scale"] * k / (k @ k)
+    case["q"] = bf16(q)
+
+
+def assert_attention_tight(got, case, fmt, tiles, what=""):
+    """As ``assert_attention``, but what is held in few bits counts by each
+    key's own weight and value (``kv8.held_terms``) and not by the request's
+    largest scale: a page of small values that has a row's weight to itself
+    has to come out as exactly as any other.  The tcgen05 form rounds a V value
+    twice to fp16, 2^-10 of itself, which the 2^-9 A leaves room for beside
+    its weights' 2^-11."""
+    want, A, X, _ = kv8.tree_attention(case, fmt)
+    tol = 2.0 ** -8 * np.abs(want) + A * (2.0 ** -8 + 2.0 ** -9 + 2 * case["D"] * 2.0 ** -23 * X[:, :, None]) + \
+        kv8.held_terms(case, fmt, tiles) + 1e-30
+    err = np.abs(got - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} elements off, worst {np.nanmax(err / tol):.2f} of the bound"

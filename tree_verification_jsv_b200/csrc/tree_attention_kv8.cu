@@ -548,8 +548,8 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             const float mw = m_sh[w][row], lw = l_sh[w][row];
-            if (mw == -INFINITY && lw == 0.f) continue;          // saw nothing
-            const float f = mw == -INFINITY ? 1.f : fast_exp2(mw - M);
+            // -inf: saw nothing (0), or NaN in what it saw (1)
+            const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : fast_exp2(mw - M);
             const float4 v = *reinterpret_cast<const float4 *>(smem + w * L::kWarp + (row * D + 4 * c) * 4);
             acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
@@ -621,7 +621,8 @@ kv8_merge_kernel(const Kv8Params p) {
     float o[kPer] = {};
     // eight splits' loads in flight at a time: no branch on a weight between
     // them (every split of the request has written its row); one after the
-    // other, 37 splits took 15 us
+    // other, 37 splits took 15 us.  A weight that has underflowed to zero still
+    // multiplies its row, so that an infinity or NaN in it is not lost
     const float *po = p.ws_o + row_id * D + lane * kPer;
     for (int s0 = 0; s0 < S; s0 += 8) {
         float v[8][kPer];
@@ -645,7 +646,7 @@ kv8_merge_kernel(const Kv8Params p) {
             const int s = s0 + i;
             const float w = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) o[x] = w == 0.f ? o[x] : fmaf(w, v[i][x], o[x]);
+            for (int x = 0; x < kPer; ++x) o[x] = fmaf(w, v[i][x], o[x]);
         }
     }
     const float inv = lsum == 0.f ? 0.f : 1.f / lsum;

@@ -839,6 +839,7 @@ kv8_tiles_kernel(const Kv8Params p) {
         float4 *other = reinterpret_cast<float4 *>(sKV);             // [D / 4][128 rows]
         float2 *other_ml = reinterpret_cast<float2 *>(sKV + kGroupRows * D * 4);
         float mine = vref, theirs = 0.f;                             // factors of the two groups' O
+        const bool add = dual && ntiles > 1;                         // with a factor that underflowed to zero too
         if (dual) {
             named_barrier(1, kGroups * 128);
             if (grp == 1) {
@@ -861,9 +862,9 @@ kv8_tiles_kernel(const Kv8Params p) {
             named_barrier(1, kGroups * 128);
             if (grp == 0) {
                 const float2 ml = other_ml[grow];
-                if (ntiles > 1 && !(ml.x == -INFINITY && ml.y == 0.f)) {
+                if (add) {
                     const float M = fmaxf(m_used, ml.x);
-                    theirs = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+                    theirs = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
                     const float f = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_used - M);
                     mine *= f;
                     l = l * f + ml.y * theirs;
@@ -879,7 +880,6 @@ kv8_tiles_kernel(const Kv8Params p) {
         float4 *scr = reinterpret_cast<float4 *>(sQ + grp * L::kQGroup + sub * (32 * kScrCols * 4));
         if (have_o) tc_fence_after();
         auto write_rows = [&](long long my_off, float scale, auto store) {
-            const bool add = __any_sync(0xffffffffu, theirs != 0.f);
             const float s0 = mine * scale, s1 = theirs * scale;
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
