@@ -319,7 +319,8 @@ JSV_API jsv_status jsv_lmhead_argmax_noalloc(const uint16_t *hidden, const uint1
  * Both tables are indexed by logical page (slot / 16); jsv_batch.page_table
  * entries below floor(P_b / 16) are not read, so their bf16 pages may be
  * freed or shared out again.  A value is code * scale; scales are not
- * negative, and V scales below 1e-37 may count as zero.
+ * negative, and V scales below 1e-37, or below 2^-64 of another of the same
+ * request and head, may count as zero.
  * Layout: codes [num_pages][Hkv][16][D] (the 16 x D block of one page and
  * head is contiguous), scales [num_pages][Hkv].
  * The pages that the README's engine keeps are bf16; this is a deployment
@@ -350,7 +351,11 @@ JSV_API size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, con
  * full pages are read from the 8-bit cache (the last, partial page and the
  * tree's own slots from the bf16 caches).  One node per request (node 0
  * alone) is ordinary single-token decoding.  Scores, softmax statistics and
- * the output are accumulated in fp32; the output is rounded to bf16.
+ * the output are accumulated in fp32; the output is rounded to bf16.  In the
+ * products the weight of a key of an 8-bit page is held to 2^-11 of itself or
+ * 2^-25 of the row's largest weight, whichever is more, and a V value to 2^-10
+ * of itself and 2^-29 of the largest V scale among the eight pages of its 128
+ * slots; weights of bf16 pages are rounded to bf16.
  *   q, scale, out, stream   as for jsv_tree_attention
  *   k_cache, v_cache        the bf16 caches (batch->num_pages pages)
  *   workspace, workspace_bytes  device scratch of at least

@@ -105,3 +105,44 @@ def tree_attention(case, fmt):
                     out[s0:s0 + n, h][(sees.astype(np.int64) @ odd) > 0] = np.nan
                     top[s0:s0 + n, h] = case["scale"] * np.where(sees, np.abs(qh) @ np.abs(K).T, 0).max(axis=1)
     return out, mag, top, codes
+
+
+def held_terms(case, fmt, tiles):
+    """For each output, what the 8-bit keys' weights and values may be off by
+    beyond roundings relative to themselves, as [T][Hq][D].  With w_j the
+    weight of key j relative to the row's largest and top the largest V scale
+    of the eight pages of a 128-slot tile:
+      streaming form   sum_j min(w_j, 2^-25) |v_j| / sum_j w_j
+      tcgen05 form     sum_j (min(w_j, 2^-31) |v_j| + w_j 2^-28 top_j) / sum_j w_j"""
+    Hq, Hkv, D = case["Hq"], case["Hkv"], case["D"]
+    G, offs = Hq // Hkv, case["node_offsets"]
+    out = np.zeros((int(offs[-1]), Hq, D))
+    q = bf16_to_f64(case["q"])
+    kc = bf16_to_f64(case["k_cache"])
+    for b in range(len(offs) - 1):
+        s0, n, P = int(offs[b]), int(offs[b + 1] - offs[b]), int(case["prefix_len"][b])
+        full = P // PAGE
+        pg8 = case["page_table8"][b, :full]
+        slots = np.arange(full * PAGE, P + n)
+        pg = case["page_table"][b][slots // PAGE]
+        sees = np.zeros((n, P + n), dtype=bool)
+        sees[:, :P] = True
+        for i in range(n):
+            j = i
+            while j >= 0:
+                sees[i, P + j] = True
+                j = int(case["parent"][s0 + j])
+        for g in range(Hkv):
+            ks, vs = (case[x][pg8, g].astype(np.float64) for x in ("k_scale", "v_scale"))
+            K = np.concatenate([(decode(case["k8"][pg8, g], fmt) * ks[:, None, None]).reshape(-1, D), kc[pg, slots % PAGE, g]])
+            V = np.abs(decode(case["v8"][pg8, g], fmt) * vs[:, None, None]).reshape(-1, D)
+            top = np.repeat([vs[i // 8 * 8:i // 8 * 8 + 8].max() for i in range(full)], PAGE)
+            for h in range(g * G, (g + 1) * G):
+                s = np.where(sees, case["scale"] * (q[s0:s0 + n, h] @ K.T), -np.inf)
+                w = np.exp(s - s.max(axis=1, keepdims=True))
+                total, w = w.sum(axis=1, keepdims=True), w[:, :full * PAGE]
+                off = np.minimum(w, 2.0 ** (-31 if tiles else -25)) @ V
+                if tiles and full:
+                    off = off + 2.0 ** -28 * (w @ top)[:, None]
+                out[s0:s0 + n, h] = off / total
+    return out

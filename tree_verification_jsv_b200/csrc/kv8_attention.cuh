@@ -18,6 +18,11 @@ constexpr int kTreeWords = kMaxTreeNodes / 32;
 constexpr float kMaxSlack = 8.f;             // log2 units a score may pass the running maximum by
 constexpr float kWeightShift = 64.f;         // 2^6: weights are held as 2^6 e vs / vref in fp16
 constexpr int kMaxSplits = 64;
+// V scales up to 1e-37 count as zero (the reciprocal of a reference scale stays
+// finite), and none is taken as the reference below 2^-64 of the largest before
+// it (an accumulator of 2^45 stays finite when it is rescaled by as much).
+constexpr float kMinScale = 1.0e-37f;
+constexpr float kScaleRange = 5.421010862427522e-20f;
 
 struct Kv8Params {
     BatchArgs a;
@@ -55,6 +60,13 @@ __device__ __forceinline__ int unit_tile(int u, int pre_tiles) {
 }
 // Splits of a request of `units`: about C units each, at most S.
 __device__ __forceinline__ int unit_splits(int units, int C, int S) { return max(1, min(S, (units + C - 1) / C)); }
+
+// 1 / x to 2^-23 over the whole range of x, without a division's code.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Two fp16 from two fp32, the first in the low half.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

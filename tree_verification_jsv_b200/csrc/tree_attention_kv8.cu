@@ -13,11 +13,15 @@
 // bits, 2^-11 of each weight; bf16 output rounds by 2^-8).
 //
 // Weights of pages with different V scales share one accumulator through a
-// reference scale vref: a weight is stored as 2^6 e_j vs / vref.  With
-// e_j <= 2^8 and vs <= 2 vref it stays below 2^15, inside fp16; the
-// accumulator is rescaled when a page's scale passes 2 vref.  The running
-// maximum m moves only when a score passes it by 8 (2^8), so most pages need
-// no reduction over the row.
+// reference scale vref: a weight is stored as 2^6 e_j vs / vref.  The reference
+// follows the pages' scales up and down: vref is set to a page's scale, and the
+// accumulator rescaled, where the scale lies outside vref * [2^-6, 2].  With
+// e_j <= 2^8 a stored weight stays below 2^15, inside fp16, and its step there,
+// 2^-24 below 2^-14, is at most 2^-25 2^-6 2^6 = 2^-25 of vs: a row whose weight
+// lies on a page of small values gets them as exactly as any others.  (A
+// reference that only grew lost such pages: 5% off at 2^-27 of the largest
+// scale, nothing left at 2^-31.)  The running maximum m moves only when a score
+// passes it by 8 (2^8), so most pages need no reduction over the row.
 #include "kv8_attention.cuh"
 
 #include <algorithm>
@@ -268,7 +272,8 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
 
     // o[nt][i][c + 2 d]: row 2t + c, dim n*D/8 + 2i + d
-    float o[NT][kTiles][4], m[NT][2], l[NT][2], vref = 0.f;
+    float o[NT][kTiles][4], m[NT][2], l[NT][2];
+    float vmul = 0.f, vtop = 0.f;                // 2^6 / vref (0: none yet), the largest reference so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -319,18 +324,22 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 l[nt][c] += sc[nt][c] + sc[nt][c + 2];
             }
     };
-    // the reference scale takes in a page's (or, for bf16 values, 1)
+    // The reference scale follows a page's (or, for bf16 values, 1), but stays
+    // within kScaleRange of the largest, so that the accumulator stays in fp32.
     auto take_scale = [&](float vs) -> float {
-        if (fabsf(vs) > 2.f * vref) {
-            const float f = vref / fabsf(vs);
+        const float w = fabsf(vs) * vmul;            // 2^6 vs / vref
+        if ((w < 1.f || w > 2.f * kWeightShift) && fabsf(vs) > kMinScale) {
+            vtop = fmaxf(vtop, fabsf(vs));
+            const float inv = fast_rcp(fmaxf(fmaxf(fabsf(vs), 1.0e-36f), vtop * kScaleRange));
+            const float f = vmul == 0.f ? 0.f : kWeightShift * inv * fast_rcp(vmul);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 scale_o(nt, 0, f);
                 scale_o(nt, 1, f);
             }
-            vref = fabsf(vs);
+            vmul = kWeightShift * inv;
         }
-        return vref > 0.f ? __fdividef(vs, vref) * kWeightShift : vs * 0.f;
+        return vs * vmul;
     };
 
     bool ok = true;
@@ -514,8 +523,9 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
     }
 
-    // This warp's rows, in fp32 and without the reference scale, over its ring
-    const float undo = vref / kWeightShift;
+    // This warp's rows, in fp32, without the reference scale and divided by their
+    // own sum (averages of V: a sum of large values might not be finite), over
+    // its ring
     float *mine = reinterpret_cast<float *>(ring);
     __syncwarp();
 #pragma unroll
@@ -526,6 +536,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             float sum = l[nt][c];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const float undo = vmul == 0.f ? 0.f : fast_rcp(vmul) * (sum == 0.f ? 1.f : fast_rcp(sum));
             if (n == 0) {
                 m_sh[warp][row] = ok ? m[nt][c] : -INFINITY;
                 l_sh[warp][row] = ok ? sum : 0.f;
@@ -543,25 +554,28 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, m_sh[w][row]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
+        float wt[kRowWarps], lsum = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             const float mw = m_sh[w][row], lw = l_sh[w][row];
-            // -inf: saw nothing (0), or NaN in what it saw (1)
-            const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : fast_exp2(mw - M);
+            // -inf: saw nothing, or NaN in what it saw
+            wt[w] = lw == 0.f ? 0.f : mw == -INFINITY ? lw : fast_exp2(mw - M) * lw;
+            lsum += wt[w];
+        }
+        const float inv = lsum == 0.f ? 0.f : fast_rcp(lsum);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+            const float f = wt[w] * inv;
             const float4 v = *reinterpret_cast<const float4 *>(smem + w * L::kWarp + (row * D + 4 * c) * 4);
             acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
-            lsum = fmaf(f, lw, lsum);
         }
         const size_t row_id = (size_t)(r.base + rg / G) * a.Hq + g * G + rg % G;
         if (Sb == 1) {
-            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
             const size_t oi = row_id * D + 4 * c;
             if (JSV_IN_BOUNDS(oi + 3, (long long)rows * D, a.dev_status))
-                *reinterpret_cast<uint2 *>(p.out + oi) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                                                    pack_bf16x2(acc.z * inv, acc.w * inv));
+                *reinterpret_cast<uint2 *>(p.out + oi) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         } else {
             const size_t part = (size_t)split * rows + row_id;
             if (JSV_IN_BOUNDS(part, (long long)p.S * rows, a.dev_status)) {
@@ -609,14 +623,17 @@ kv8_merge_kernel(const Kv8Params p) {
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float f[2], lsum = 0.f;
+    float f[2], lsum = 0.f;                      // weights of the splits' rows
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        f[k] = ls[k] == 0.f ? 0.f : ms[k] == -INFINITY ? 1.f : fast_exp2(ms[k] - M);
-        lsum = fmaf(f[k], ls[k], lsum);
+        f[k] = ls[k] == 0.f ? 0.f : ms[k] == -INFINITY ? ls[k] : fast_exp2(ms[k] - M) * ls[k];
+        lsum += f[k];
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) f[k] *= inv;
     constexpr int kPer = D / 32;
     float o[kPer] = {};
     // eight splits' loads in flight at a time: no branch on a weight between
@@ -649,10 +666,9 @@ kv8_merge_kernel(const Kv8Params p) {
             for (int x = 0; x < kPer; ++x) o[x] = fmaf(w, v[i][x], o[x]);
         }
     }
-    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
     uint32_t *out = reinterpret_cast<uint32_t *>(p.out + row_id * D + lane * kPer);
 #pragma unroll
-    for (int x = 0; x < kPer; x += 2) out[x / 2] = pack_bf16x2(o[x] * inv, o[x + 1] * inv);
+    for (int x = 0; x < kPer; x += 2) out[x / 2] = pack_bf16x2(o[x], o[x + 1]);
 }
 
 // ---------------------------------------------------------------------------

@@ -26,11 +26,16 @@
 //
 // The K scale of a page multiplies its 16 score columns (it rides on the
 // multiply that brings scores to log2 units).  The V scale goes into the
-// fp16 V tile as vs / vref, a rounding of 2^-10 of each value, instead of
-// into the weights: the converting warps have the instructions to spare, the
-// softmax warps do not.  vref is the CTA's reference scale; it changes only
-// when a page's scale passes 2 vref, and then O is rescaled with the running
-// maximum's correction.
+// fp16 V tile as vs / vref, instead of into the weights: the converting warps
+// have the instructions to spare, the softmax warps do not.  vref is the CTA's
+// reference scale.  It follows the tiles' largest V scales up and down, so that
+// such a page's factor lies in [16, 128], from the middle of fp16's normal
+// range to where 448 times it still is finite; where it changes, O is rescaled
+// with the running maximum's correction.  A factor below 2^-14 is applied in
+// two steps, 2^14 times as large and then by 2^-14, so that it is never
+// rounded as a subnormal number.  A value is off by two roundings, 2^-10 of it,
+// and, below 2^-14 in units of vref, by fp16's step there: by up to 2^-25 vref,
+// which is 2^-29 of the largest V scale of its tile.
 //
 // A tile took about 4,300 cycles when 256 nodes over 16384 tokens took 118 us
 // (timeline of one CTA): softmax about 2,400 (scores from TMEM 230, maximum 450,
@@ -69,6 +74,8 @@ constexpr int kRegsMma = 80;
 constexpr int kRegsSoftmax = 176;
 constexpr int kSlots = 4;                        // tiles whose scales are held, see TileInfo
 constexpr float kWeightLog2 = 6.f;               // weights are held as 2^6 e: e <= 2^8 stays inside fp16
+constexpr float kTinyRatio = 6.103515625e-05f;   // 2^-14, the smallest normal fp16 number,
+constexpr uint32_t kTinyPair = 0x04000400u;      // and a pair of them
 
 // What the softmax warps need of a tile.  Written before the tile's K is
 // handed over and once its place in the ring is free: by then S of tile j - 2
@@ -346,7 +353,7 @@ kv8_tiles_kernel(const Kv8Params p) {
                              "l"(codes + ((size_t)pages * a.Hkv + g) * kBlock), "r"(kBlock), "r"(smem_addr(landed))
                              : "memory");
         };
-        auto store = [&](uint8_t *tile, int pages, uint32_t ratios) {
+        auto store = [&](uint8_t *tile, int pages, uint32_t ratios, uint32_t tiny) {
             const int chunk = (cc & 3) * 2;
 #pragma unroll 1
             for (int pg = me; pg < kTilePages; pg += kTeam) {
@@ -379,6 +386,22 @@ kv8_tiles_kernel(const Kv8Params p) {
                     }
                 }
             }
+            // the second step of tiny factors, by the lanes that stored the values
+            // (a branch for it in the loop above cost 0.4%)
+            if (is_v && tiny) {
+#pragma unroll 1
+                for (int i = me * kUnits; i < kTilePages * kUnits; i += (i + 1) % kUnits ? 1 : 1 + (kTeam - 1) * kUnits) {
+                    if (!((tiny >> (i / kUnits)) & 1)) continue;
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        uint4 *at = reinterpret_cast<uint4 *>(tile + (i & ~1) * (kUnitRows * 128) +
+                                                              sw128_offset((i & 1) * kUnitRows + urow, chunk + k));
+                        const uint4 x = *at;
+                        *at = make_uint4(mul_f16x2(x.x, kTinyPair), mul_f16x2(x.y, kTinyPair), mul_f16x2(x.z, kTinyPair),
+                                         mul_f16x2(x.w, kTinyPair));
+                    }
+                }
+            }
         };
         // every thread's stores, then one arrival a warp
         auto hand_over = [&](uint64_t *bar) {
@@ -402,14 +425,15 @@ kv8_tiles_kernel(const Kv8Params p) {
             return wait_for(&empty[j % kStages], ((j / kStages) & 1) ^ 1) && (!is_v || j != 1 || wait_for(&tree_read, 0));
         };
 
-        // Both teams keep the same reference.  Its reciprocal stays finite: values
-        // of a scale below 1e-37 count as zero.  (A division here or in the
-        // softmax, with the code of its rare cases, cost 6%.)
-        float vref = 0.f, vinv = 0.f;
-        auto take_scale = [&](float vs) {                    // largest scale of a tile
-            if (vs > 2.f * vref && vs > 1.0e-37f) {
-                vref = vs;
-                vinv = 1.f / vs;
+        // Both teams keep the same reference, `want` where that lies outside
+        // vref * [1/4, 2].  (A division here or in the softmax, with the code of
+        // its rare cases, cost 6%.)
+        float vref = 0.f, vinv = 0.f, vtop = 0.f;
+        auto refer = [&](float want) {
+            if (want > 2.f * vref || want < 0.25f * vref) {
+                vtop = fmaxf(vtop, want);
+                vref = fmaxf(want, vtop * kScaleRange);
+                vinv = 1.f / vref;
             }
         };
         // page numbers two tiles ahead, scales one: neither is waited for
@@ -433,8 +457,11 @@ kv8_tiles_kernel(const Kv8Params p) {
             float top = fabsf(vs);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            take_scale(__shfl_sync(0xffffffffu, top, 0));
-            const float ratio = vs * vinv;
+            top = __shfl_sync(0xffffffffu, top, 0);
+            if (top > kMinScale) refer(fmaxf(top * 0.015625f, kMinScale));
+            float ratio = vs * vinv;
+            const bool tiny = fabsf(ratio) < kTinyRatio;
+            if (tiny) ratio *= 1.f / kTinyRatio;
             ok = wait_for(landed, j & 1) && stage_free(j);
             if (!ok) break;
             if (!is_v && me == 0) {
@@ -446,7 +473,7 @@ kv8_tiles_kernel(const Kv8Params p) {
                     ti.vinv = vinv;
                 }
             }
-            store(tiles + (j % kStages) * L::kStage, pages, pack_f16(ratio, ratio));
+            store(tiles + (j % kStages) * L::kStage, pages, pack_f16(ratio, ratio), __ballot_sync(0xffffffffu, tiny));
             hand_over(&full[j % kStages]);
             pages = pages_next;
             fetch(pages);
@@ -483,7 +510,7 @@ kv8_tiles_kernel(const Kv8Params p) {
         for (int j = n_pre; ok && j < ntiles; ++j) {
             const int slot0 = tail_slot(j);
             TileInfo &ti = info[j % kSlots];
-            take_scale(1.f);
+            refer(1.f);
             ok = stage_free(j);
             if (!ok) break;
             if (is_v) {
@@ -838,7 +865,9 @@ kv8_tiles_kernel(const Kv8Params p) {
         // are at the barrier).
         float4 *other = reinterpret_cast<float4 *>(sKV);             // [D / 4][128 rows]
         float2 *other_ml = reinterpret_cast<float2 *>(sKV + kGroupRows * D * 4);
-        float mine = vref, theirs = 0.f;                             // factors of the two groups' O
+        // Factors of the two groups' O.  Rows are handed on divided by their own
+        // sum, as averages of V: a sum of large values might not be finite.
+        float mine = l == 0.f ? vref : vref / l, theirs = 0.f;
         const bool add = dual && ntiles > 1;                         // with a factor that underflowed to zero too
         if (dual) {
             named_barrier(1, kGroups * 128);
@@ -854,8 +883,8 @@ kv8_tiles_kernel(const Kv8Params p) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             other[(c0 / 4 + x) * kGroupRows + grow] =
-                                make_float4(__uint_as_float(rr[4 * x]) * vref, __uint_as_float(rr[4 * x + 1]) * vref,
-                                            __uint_as_float(rr[4 * x + 2]) * vref, __uint_as_float(rr[4 * x + 3]) * vref);
+                                make_float4(__uint_as_float(rr[4 * x]) * mine, __uint_as_float(rr[4 * x + 1]) * mine,
+                                            __uint_as_float(rr[4 * x + 2]) * mine, __uint_as_float(rr[4 * x + 3]) * mine);
                     }
                 }
             }
@@ -864,10 +893,12 @@ kv8_tiles_kernel(const Kv8Params p) {
                 const float2 ml = other_ml[grow];
                 if (add) {
                     const float M = fmaxf(m_used, ml.x);
-                    theirs = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
-                    const float f = m_used == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_used - M);
-                    mine *= f;
-                    l = l * f + ml.y * theirs;
+                    const float w0 = l == 0.f ? 0.f : m_used == -INFINITY ? l : fast_exp2(m_used - M) * l;
+                    const float w1 = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? ml.y : fast_exp2(ml.x - M) * ml.y;
+                    l = w0 + w1;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    mine *= w0 * inv;
+                    theirs = w1 * inv;
                     m_used = M;
                 }
             }
@@ -879,8 +910,7 @@ kv8_tiles_kernel(const Kv8Params p) {
         constexpr int kScrCols = D / 2, kChunks = kScrCols / 4, kRowsPerStore = 32 / kChunks;
         float4 *scr = reinterpret_cast<float4 *>(sQ + grp * L::kQGroup + sub * (32 * kScrCols * 4));
         if (have_o) tc_fence_after();
-        auto write_rows = [&](long long my_off, float scale, auto store) {
-            const float s0 = mine * scale, s1 = theirs * scale;
+        auto write_rows = [&](long long my_off, auto store) {
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
@@ -895,12 +925,12 @@ kv8_tiles_kernel(const Kv8Params p) {
                     }
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        float4 v = make_float4(__uint_as_float(rr[4 * x]) * s0, __uint_as_float(rr[4 * x + 1]) * s0,
-                                               __uint_as_float(rr[4 * x + 2]) * s0, __uint_as_float(rr[4 * x + 3]) * s0);
+                        float4 v = make_float4(__uint_as_float(rr[4 * x]) * mine, __uint_as_float(rr[4 * x + 1]) * mine,
+                                               __uint_as_float(rr[4 * x + 2]) * mine, __uint_as_float(rr[4 * x + 3]) * mine);
                         if (add) {
                             const float4 u = other[((pass * kScrCols + c0) / 4 + x) * kGroupRows + grow];
-                            v.x = fmaf(u.x, s1, v.x), v.y = fmaf(u.y, s1, v.y);
-                            v.z = fmaf(u.z, s1, v.z), v.w = fmaf(u.w, s1, v.w);
+                            v.x = fmaf(u.x, theirs, v.x), v.y = fmaf(u.y, theirs, v.y);
+                            v.z = fmaf(u.z, theirs, v.z), v.w = fmaf(u.w, theirs, v.w);
                         }
                         scr[lane * kChunks + ((c0 / 4 + x) ^ (lane & (kChunks - 1)))] = v;
                     }
@@ -919,14 +949,14 @@ kv8_tiles_kernel(const Kv8Params p) {
         if (dual && grp == 1) {
             // merged into the first group's rows
         } else if (Sb == 1) {
-            write_rows(row_valid ? (long long)(row_id * D) : -1ll, l == 0.f ? 0.f : 1.f / l,
+            write_rows(row_valid ? (long long)(row_id * D) : -1ll,
                        [&](long long o, const float4 &v) {
                            if (JSV_IN_BOUNDS(o + 3, (long long)rows * D, a.dev_status))
                                *reinterpret_cast<uint2 *>(p.out + o) = make_uint2(pack_bf16x2(v.x, v.y),
                                                                                   pack_bf16x2(v.z, v.w));
                        });
         } else {
-            write_rows(row_valid ? (long long)(((size_t)split * rows + row_id) * D) : -1ll, 1.f,
+            write_rows(row_valid ? (long long)(((size_t)split * rows + row_id) * D) : -1ll,
                        [&](long long o, const float4 &v) {
                            if (JSV_IN_BOUNDS(o + 3, (long long)p.S * rows * D, a.dev_status))
                                *reinterpret_cast<float4 *>(p.ws_o + o) = v;
