@@ -365,9 +365,12 @@ JSV_API size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, con
  *            replayed side by side included, take workspaces of their own
  * Values that a node does not see do not reach its output, whatever they are
  * (infinities and NaN in later slots of a page and in other branches of the
- * tree included).  A node that sees a non-finite K or V value, or a
- * non-finite scale, gets non-finite outputs (a visible non-finite value in
- * the bf16 V cache makes all of the head's output NaN).
+ * tree included).  A node that sees a non-finite V value or scale, however
+ * small its weight, gets non-finite outputs (a visible non-finite value in the
+ * bf16 V cache makes all of the head's output NaN); so does one that sees a
+ * NaN in K or a non-finite K scale.  An infinity in the bf16 K cache counts by
+ * its score: plus infinity gives NaN, minus infinity a weight of zero, and NaN
+ * where no score of the node is finite.
  * Supported: D in {64, 128}; prefix pages need a row in each table.  The
  * codes of a request's pages are trusted; page indices are checked.
  */

@@ -155,7 +155,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (page >= 0 && page < p.c.num_pages) {
                 const size_t block = (size_t)page * a.Hkv + g;
                 row = (int)block * 16;
-                ks = __ldg(p.c.k_scale + block);
+                ks = finite_or_nan(__ldg(p.c.k_scale + block));
                 vs = __ldg(p.c.v_scale + block);
             } else {
                 flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
@@ -562,7 +562,9 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             wt[w] = lw == 0.f ? 0.f : mw == -INFINITY ? lw : fast_exp2(mw - M) * lw;
             lsum += wt[w];
         }
-        const float inv = lsum == 0.f ? 0.f : fast_rcp(lsum);
+        // no weight at all (every score -inf): NaN, but a split's row leaves that
+        // to the others
+        const float inv = lsum == 0.f && Sb > 1 ? 0.f : fast_rcp(lsum);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
@@ -631,7 +633,7 @@ kv8_merge_kernel(const Kv8Params p) {
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
-    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+    const float inv = 1.f / lsum;                // no weight at all: 0 * inf, NaN
 #pragma unroll
     for (int k = 0; k < 2; ++k) f[k] *= inv;
     constexpr int kPer = D / 32;

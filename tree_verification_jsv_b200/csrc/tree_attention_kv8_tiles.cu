@@ -443,7 +443,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             ks = vs = 0.f;
             if (pages >= 0) {
                 const size_t block = (size_t)pages * a.Hkv + g;
-                if constexpr (!is_v) ks = __ldg(p.c.k_scale + block);
+                if constexpr (!is_v) ks = finite_or_nan(__ldg(p.c.k_scale + block));
                 vs = __ldg(p.c.v_scale + block);
             }
         };
@@ -949,6 +949,7 @@ kv8_tiles_kernel(const Kv8Params p) {
         if (dual && grp == 1) {
             // merged into the first group's rows
         } else if (Sb == 1) {
+            if (l == 0.f) mine = __uint_as_float(0x7fc00000u);       // no weight at all: every score -inf
             write_rows(row_valid ? (long long)(row_id * D) : -1ll,
                        [&](long long o, const float4 &v) {
                            if (JSV_IN_BOUNDS(o + 3, (long long)rows * D, a.dev_status))
