@@ -322,7 +322,7 @@ JSV_API jsv_status jsv_lmhead_argmax_noalloc(const uint16_t *hidden, const uint1
  * negative, and V scales below 1e-37, or below 2^-64 of another of the same
  * request and head, may count as zero.
  * Layout: codes [num_pages][Hkv][16][D] (the 16 x D block of one page and
- * head is contiguous), scales [num_pages][Hkv].
+ * head is contiguous), scales [num_pages][Hkv]; num_pages * Hkv * 16 < 2^31.
  * The pages that the README's engine keeps are bf16; this is a deployment
  * form of the same cache with half its bytes.  Device pointers of these and
  * the page pool's calls belong to the current device, whose stream is given.
@@ -371,8 +371,9 @@ JSV_API size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, con
  * NaN in K or a non-finite K scale.  An infinity in the bf16 K cache counts by
  * its score: plus infinity gives NaN, minus infinity a weight of zero, and NaN
  * where no score of the node is finite.
- * Supported: D in {64, 128}; prefix pages need a row in each table.  The
- * codes of a request's pages are trusted; page indices are checked.
+ * Supported: D in {64, 128}, B * Hkv <= 65535; prefix pages need a row in
+ * each table.  The codes of a request's pages are trusted; page indices are
+ * checked.
  */
 JSV_API jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
                                           const uint16_t *k_cache, const uint16_t *v_cache, float scale,
@@ -397,7 +398,7 @@ JSV_API jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 
  * whose entry is out of range, is flagged (JSV_ERR_DEVICE_INPUT) and skipped.
  * Two requests must not write the same 8-bit page in one call; one that asks
  * for more pages than the cache has is flagged and writes nothing.
- * Supported: B <= JSV_PAGES_MAX_ROWS.
+ * Supported: B <= JSV_PAGES_MAX_ROWS, B * cache8->max_pages_per_req < 2^31.
  *   from_len, to_len   device [B] int32 (from_len may be NULL)
  */
 #define JSV_PAGES_MAX_ROWS 8192

@@ -24,19 +24,6 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// What the 8-bit cache's calls use of the structure beside a checked batch.
-jsv_status check_kv8(const jsv_batch *b, const jsv_kv8 *c) {
-    if (!c) return JSV_ERR_INVALID_ARG;
-    if (c->num_pages < 1 || c->max_pages_per_req < 1) return JSV_ERR_INVALID_ARG;
-    if (c->format != JSV_KV8_E4M3 && c->format != JSV_KV8_INT8) return JSV_ERR_UNSUPPORTED;
-    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table) return JSV_ERR_INVALID_ARG;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return JSV_ERR_INVALID_ARG;
-    // rows of the code arrays are 32-bit coordinates of the copies
-    if ((long long)c->num_pages * b->Hkv * 16 > 0x7fffffff) return JSV_ERR_UNSUPPORTED;
-    if ((long long)b->B * b->Hkv > 65535) return JSV_ERR_UNSUPPORTED;    // a grid dimension
-    return JSV_OK;
-}
-
 jsv_status check_pool(const jsv_page_pool *p, const void *table, int32_t B, int32_t max_pages) {
     if (!p || !p->refcount || !table || p->num_pages < 1 || B < 1 || max_pages < 1) return JSV_ERR_INVALID_ARG;
     // slot counts of a row are 32-bit
@@ -60,6 +47,27 @@ jsv_status check_batch(const jsv_batch *b) {
     if ((long long)b->max_pages_per_req * b->page_size < 1) return JSV_ERR_INVALID_ARG;
     if (!b->page_table || !b->prefix_len || !b->node_offsets || !b->parent) return JSV_ERR_INVALID_ARG;
     return JSV_OK;
+}
+
+// What the 8-bit cache's calls use of the structure beside a checked batch.
+jsv_status check_kv8(const jsv_batch *b, const jsv_kv8 *c) {
+    if (!c) return JSV_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->max_pages_per_req < 1) return JSV_ERR_INVALID_ARG;
+    if (c->format != JSV_KV8_E4M3 && c->format != JSV_KV8_INT8) return JSV_ERR_UNSUPPORTED;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table) return JSV_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return JSV_ERR_INVALID_ARG;
+    // rows of the code arrays are 32-bit coordinates of the copies
+    if ((long long)c->num_pages * b->Hkv * 16 > 0x7fffffff) return JSV_ERR_UNSUPPORTED;
+    return JSV_OK;
+}
+
+// The attention's geometry besides: (request, KV head) is a grid dimension.
+jsv_status check_attention_kv8(const jsv_batch *b, const jsv_kv8 *c) {
+    jsv_status s = check_batch(b);
+    if (s != JSV_OK) return s;
+    s = check_kv8(b, c);
+    if (s != JSV_OK) return s;
+    return (long long)b->B * b->Hkv > 65535 ? JSV_ERR_UNSUPPORTED : JSV_OK;
 }
 
 }  // namespace
@@ -186,16 +194,14 @@ jsv_status jsv_accum_logp_tree(const float *logp, const int32_t *topk_tokens, co
 }
 
 size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, const jsv_kv8 *cache8) {
-    if (check_batch(batch) != JSV_OK || check_kv8(batch, cache8) != JSV_OK) return 0;
+    if (check_attention_kv8(batch, cache8) != JSV_OK) return 0;
     return jsv::attention_kv8_workspace_bytes(jsv::to_args(batch), *cache8);
 }
 
 jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
                                   const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,
                                   void *workspace, size_t workspace_bytes, void *stream) {
-    jsv_status s = check_batch(batch);
-    if (s != JSV_OK) return s;
-    s = check_kv8(batch, cache8);
+    const jsv_status s = check_attention_kv8(batch, cache8);
     if (s != JSV_OK) return s;
     if (!q || !k_cache || !v_cache || !out) return JSV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
