@@ -356,7 +356,7 @@ JSV_API size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, con
  * 2^-25 of the row's largest weight, whichever is more, and a V value to 2^-10
  * of itself and 2^-29 of the largest V scale among the eight pages of its 128
  * slots; weights of bf16 pages are rounded to bf16.
- *   q, scale, out, stream   as for jsv_tree_attention
+ *   q, scale, out, stream   as for jsv_tree_attention (scale <= 2.3e38)
  *   k_cache, v_cache        the bf16 caches (batch->num_pages pages)
  *   workspace, workspace_bytes  device scratch of at least
  *            jsv_tree_attention_kv8_workspace_size() bytes, 256-B aligned

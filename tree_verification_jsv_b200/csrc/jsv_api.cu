@@ -206,7 +206,8 @@ jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8,
     if (!q || !k_cache || !v_cache || !out) return JSV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
         return JSV_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale > 3.0e38f) return JSV_ERR_INVALID_ARG;
+    // scale * log2(e) is to be finite
+    if (!(scale > 0.f) || scale > 2.3e38f) return JSV_ERR_INVALID_ARG;
     const jsv::BatchArgs a = jsv::to_args(batch);
     const size_t need = jsv::attention_kv8_workspace_bytes(a, *cache8);
     if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 256)))) return JSV_ERR_INVALID_ARG;
