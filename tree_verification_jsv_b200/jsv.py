@@ -159,8 +159,13 @@ def _addr(x) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        if torch.cuda.is_initialized():      # the current stream's handle, without an object around it
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if torch.cuda.is_initialized():
+            # the current stream's handle without an object around it (5 us a
+            # call less), by names that a version of torch may lack
+            try:
+                return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            except AttributeError:
+                pass
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
