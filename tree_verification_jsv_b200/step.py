@@ -32,6 +32,12 @@ def _i32(x, device):
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32)).to(device)
 
 
+def _on(stream):
+    """Torch's current stream for a while: a torch stream, a raw handle, or None
+    for the one that is current already."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _bf16(bits, device):
     t = torch.from_numpy(np.ascontiguousarray(bits, dtype=np.uint16).view(np.int16))
     return t.view(torch.bfloat16).to(device)
@@ -179,11 +185,12 @@ class VerifyStep:
 
     def run_host(self, stream=None):
         """Copy the input arena host->device, run the step, copy the output
-        arena back (one copy each way); returns pinned host views of path,
-        accept_len, bonus and new_len."""
-        self._in.dev_buf.copy_(self._in.host_buf, non_blocking=True)
-        self.run(stream)
-        self._out.host_buf.copy_(self._out.dev_buf, non_blocking=True)
+        arena back (one copy each way), all on ``stream``; returns pinned host
+        views of path, accept_len, bonus and new_len."""
+        with _on(stream):
+            self._in.dev_buf.copy_(self._in.host_buf, non_blocking=True)
+            self.run(stream)
+            self._out.host_buf.copy_(self._out.dev_buf, non_blocking=True)
         return self._out.host
 
     def capture_host(self):
@@ -281,9 +288,10 @@ class VerifyStepKv8(VerifyStep):
         which live on the device: of the pinned inputs, what follows them is
         copied up."""
         at = self._in.layout["node_offsets"][0]
-        self._in.dev_buf[at:].copy_(self._in.host_buf[at:], non_blocking=True)
-        self.run(stream)
-        self._out.host_buf.copy_(self._out.dev_buf, non_blocking=True)
+        with _on(stream):
+            self._in.dev_buf[at:].copy_(self._in.host_buf[at:], non_blocking=True)
+            self.run(stream)
+            self._out.host_buf.copy_(self._out.dev_buf, non_blocking=True)
         return self._out.host
 
     def h2d_bytes(self) -> int:
