@@ -230,6 +230,11 @@ class VerifyStepKv8(VerifyStep):
     for the next tree are mapped, all on the stream, so that the caller only
     writes the next tree's K/V and runs again.  A prefix may grow by as much as
     the page table's row holds.
+
+    The page tables, the prefix lengths and the trees' sizes live on the device,
+    where ``advance`` turns them over; ``host_inputs`` has the others (parent,
+    tokens, q, hidden).  Trees of other sizes (as many nodes in all) are
+    announced to ``advance``, which maps their pages.
     """
 
     def __init__(self, wl, tokens, fmt="e4m3", device="cuda", max_path=None):
@@ -270,12 +275,19 @@ class VerifyStepKv8(VerifyStep):
         jsv.jsv_tree_attention_kv8(self.batch, self.cache8, self.q, self.k_cache, self.v_cache, self.scale, self.out,
                                    self.attn_ws, stream=stream)
 
-    def advance(self, stream=None):
+    def advance(self, stream=None, node_offsets=None):
         """The turn to the next step: ``prefix_len`` becomes ``new_len``.
-        ``stream``: a torch stream, the one the step ran on, or None for the
-        current one."""
-        with torch.cuda.stream(stream):
+        ``stream``: the one the step ran on, or None for the current one.
+        ``node_offsets``: where the next trees' sizes differ, their [B + 1]
+        offsets, on the host (checked here) or on the device (checked by the
+        next step's kernels)."""
+        if node_offsets is not None:
+            node_offsets = self._checked_offsets(node_offsets)
+        with _on(stream):
             self._write_full_pages(self.prefix_len, self.new_len, stream)
+            if node_offsets is not None:
+                self.node_offsets.copy_(node_offsets, non_blocking=True)
+                torch.sub(self.node_offsets[1:], self.node_offsets[:-1], out=self.nodes)
             jsv.jsv_pages_trim(self.pool, self.page_table, self.B, self.width, self.new_len, self.new_len,
                                stream=stream)
             self.prefix_len.copy_(self.new_len)
@@ -283,11 +295,30 @@ class VerifyStepKv8(VerifyStep):
             jsv.jsv_pages_alloc(self.pool, self.page_table, self.B, self.width, self.new_len, self.tree_end, False,
                                 self.pages_ws, stream=stream)
 
+    def _checked_offsets(self, offs):
+        if isinstance(offs, torch.Tensor) and offs.is_cuda:
+            if offs.shape != (self.B + 1,):
+                raise ValueError(f"node_offsets: shape {tuple(offs.shape)}, not ({self.B + 1},)")
+            return offs
+        offs = np.ascontiguousarray(offs, dtype=np.int32)
+        if offs.shape != (self.B + 1,):
+            raise ValueError(f"node_offsets: shape {offs.shape}, not ({self.B + 1},)")
+        n = np.diff(offs)
+        if offs[0] != 0 or offs[-1] != self.T or n.min() < 1 or n.max() > self.batch.max_nodes:
+            raise ValueError(f"node_offsets: not {self.B} trees of 1 to {self.batch.max_nodes} nodes, {self.T} in all")
+        return torch.from_numpy(offs)
+
+    # -- end-to-end form: what follows the tables, lengths and sizes is copied --
+    def _copied(self) -> int:
+        return self._in.layout["parent"][0]
+
+    def host_inputs(self):
+        at = self._copied()
+        return {k: v for k, v in self._in.host.items() if self._in.layout[k][0] >= at}
+
     def run_host(self, stream=None):
-        """As the base class's, but for the page table and the prefix lengths,
-        which live on the device: of the pinned inputs, what follows them is
-        copied up."""
-        at = self._in.layout["node_offsets"][0]
+        """As the base class's; copies what ``host_inputs`` has."""
+        at = self._copied()
         with _on(stream):
             self._in.dev_buf[at:].copy_(self._in.host_buf[at:], non_blocking=True)
             self.run(stream)
@@ -295,4 +326,4 @@ class VerifyStepKv8(VerifyStep):
         return self._out.host
 
     def h2d_bytes(self) -> int:
-        return self._in.nbytes - self._in.layout["node_offsets"][0]
+        return self._in.nbytes - self._copied()
