@@ -104,3 +104,33 @@ def test_refused_sizes_and_what_the_host_may_write():
             st.advance(node_offsets=offs)
     for x, y in zip((st.page_table, st.page_table8, st.refcount, st.prefix_len, st.node_offsets), before):
         assert torch.equal(x, y)
+
+
+def test_bound_on_the_prefix():
+    """By a bound of its own the step gives the same results, and flags a
+    prefix that has grown past it."""
+    from tree_verification_jsv_b200.step import VerifyStepKv8
+    wl, tokens, _ = workload([90, 0, 47], TREES, 5, 300)
+    steps = [VerifyStepKv8(wl, tokens, "int8", max_prefix=m) for m in (None, 90)]
+    for st in steps:
+        st.run()
+    torch.cuda.synchronize()
+    a, b = steps
+    assert a.batch.max_prefix == wl.page_table.shape[1] * 16 - 1 and b.batch.max_prefix == 90
+    assert (a.out.float() - b.out.float()).abs().max() <= 2.0 ** -7 * a.out.float().abs().max()
+    for name in ("path", "accept_len", "bonus", "new_len"):
+        assert torch.equal(getattr(a, name), getattr(b, name))
+    for st in steps:
+        st.advance()
+        st.run()
+    torch.cuda.synchronize()
+    assert int(a.new_len.max().item()) > 91
+    assert int(a.status.item()) == 0 and int(b.status.item()) == jsv.JSV_ERR_DEVICE_INPUT
+
+
+@pytest.mark.parametrize("bound", [0, 89, 1 << 30])
+def test_refused_bounds(bound):
+    from tree_verification_jsv_b200.step import VerifyStepKv8
+    wl, tokens, _ = workload([90, 0, 47], TREES, 5, 8)
+    with pytest.raises(ValueError):
+        VerifyStepKv8(wl, tokens, max_prefix=bound)

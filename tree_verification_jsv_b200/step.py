@@ -229,7 +229,14 @@ class VerifyStepKv8(VerifyStep):
     the 8-bit cache, what the bf16 table no longer needs is freed, and pages
     for the next tree are mapped, all on the stream, so that the caller only
     writes the next tree's K/V and runs again.  A prefix may grow by as much as
-    the page table's row holds.
+    the page table's row holds, or to ``max_prefix`` where that is given (a
+    longer one is flagged): the attention shares out a request by that bound,
+    and where prefixes stay far below it the splits are too few (64 nodes over
+    2048 tokens: 23 us by their own bound, 29 by four times that).
+
+    The caches of this class are the workload's whole bf16 pool and an 8-bit
+    pool for full rows beside it.  What the 8-bit prefix saves are the bf16
+    pages that it frees in the pool, for other rows to take.
 
     The page tables, the prefix lengths and the trees' sizes live on the device,
     where ``advance`` turns them over; ``host_inputs`` has the others (parent,
@@ -237,13 +244,19 @@ class VerifyStepKv8(VerifyStep):
     announced to ``advance``, which maps their pages.
     """
 
-    def __init__(self, wl, tokens, fmt="e4m3", device="cuda", max_path=None):
+    def __init__(self, wl, tokens, fmt="e4m3", device="cuda", max_path=None, max_prefix=None):
+        width = wl.page_table.shape[1]
+        if max_prefix is None:
+            max_prefix = width * 16 - 1
+        if not wl.max_prefix <= max_prefix < width * 16:
+            raise ValueError(f"max_prefix {max_prefix}: not from the longest prefix, {wl.max_prefix}, to below the "
+                             f"{width * 16} slots of a row")
         super().__init__(wl, tokens, device, max_path)
-        dev, B, width = self.device, self.B, wl.page_table.shape[1]
+        dev, B = self.device, self.B
         self.width = width
         self.batch = jsv.make_batch(
             B=B, Hq=self.Hq, Hkv=self.Hkv, D=self.D, max_pages_per_req=width, num_pages=wl.num_pages,
-            total_nodes=self.T, max_nodes=wl.max_nodes, max_prefix=width * 16 - 1, page_table=self.page_table,
+            total_nodes=self.T, max_nodes=wl.max_nodes, max_prefix=max_prefix, page_table=self.page_table,
             prefix_len=self.prefix_len, node_offsets=self.node_offsets, parent=self.parent, dev_status=self.status)
         pages8 = B * width
         self.k8, self.v8 = (torch.zeros((pages8, self.Hkv, 16, self.D), dtype=torch.uint8, device=dev) for _ in range(2))
