@@ -380,6 +380,21 @@ JSV_API jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 
                                           uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * How jsv_tree_attention_kv8 takes a geometry on the current device, from the
+ * host-side fields of both structures: a diagnostic for tests and for the
+ * choice of bounds (a batch whose prefixes stay far below max_prefix, or a
+ * pool with many pages to spare, gets fewer splits than it could use).
+ */
+typedef struct {
+    int32_t rows;                /* query rows of a KV head that are taken together:
+                                    8 or 16 (streaming form) or 256 (tcgen05 form)     */
+    int32_t splits;              /* most splits of a request                           */
+    int32_t split_units;         /* pages (streaming) or 128-slot tiles that a split
+                                    aims at                                            */
+} jsv_kv8_plan;
+JSV_API jsv_status jsv_tree_attention_kv8_plan(const jsv_batch *batch, const jsv_kv8 *cache8, jsv_kv8_plan *plan);
+
+/*
  * Full pages of the bf16 cache written to the 8-bit cache.  For request b the
  * logical pages floor(from_len[b] / 16) .. floor(to_len[b] / 16) - 1 are read
  * through batch->page_table and written through cache8->page_table: after a

@@ -198,6 +198,14 @@ size_t jsv_tree_attention_kv8_workspace_size(const jsv_batch *batch, const jsv_k
     return jsv::attention_kv8_workspace_bytes(jsv::to_args(batch), *cache8);
 }
 
+jsv_status jsv_tree_attention_kv8_plan(const jsv_batch *batch, const jsv_kv8 *cache8, jsv_kv8_plan *plan) {
+    const jsv_status s = check_attention_kv8(batch, cache8);
+    if (s != JSV_OK) return s;
+    if (!plan) return JSV_ERR_INVALID_ARG;
+    *plan = jsv::attention_kv8_plan(jsv::to_args(batch), *cache8);
+    return JSV_OK;
+}
+
 jsv_status jsv_tree_attention_kv8(const jsv_batch *batch, const jsv_kv8 *cache8, const uint16_t *q,
                                   const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,
                                   void *workspace, size_t workspace_bytes, void *stream) {

@@ -12,6 +12,7 @@ namespace jsv {
 // swizzled by the row's width.
 bool encode_tensor_map_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_outer);
 
+jsv_kv8_plan attention_kv8_plan(const BatchArgs &a, const jsv_kv8 &c);
 size_t attention_kv8_workspace_bytes(const BatchArgs &a, const jsv_kv8 &c);
 cudaError_t launch_tree_attention_kv8(const BatchArgs &a, const jsv_kv8 &c, const uint16_t *q,
                                       const uint16_t *k_cache, const uint16_t *v_cache, float scale, uint16_t *out,

@@ -795,6 +795,11 @@ cudaError_t launch_kv8(const Kv8Params &p, int nt, cudaStream_t st) {
 
 }  // namespace
 
+jsv_kv8_plan attention_kv8_plan(const BatchArgs &a, const jsv_kv8 &c) {
+    const Kv8Plan pl = plan_of(a, c);
+    return {pl.nt ? 8 * pl.nt : 256, pl.S, pl.C};
+}
+
 size_t attention_kv8_workspace_bytes(const BatchArgs &a, const jsv_kv8 &c) {
     const Kv8Plan pl = plan_of(a, c);
     return pl.S > 1 ? (size_t)pl.S * a.total_nodes * a.Hq * ((size_t)a.D + 2) * sizeof(float) : 0;

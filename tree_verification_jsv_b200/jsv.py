@@ -73,6 +73,10 @@ class jsv_kv8(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
+class jsv_kv8_plan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("splits", ctypes.c_int32), ("split_units", ctypes.c_int32)]
+
+
 class jsv_page_pool(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("refcount", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
@@ -128,6 +132,8 @@ def load() -> ctypes.CDLL:
     lib.jsv_tree_attention_kv8_workspace_size.restype = sz
     lib.jsv_tree_attention_kv8.argtypes = [bp, kp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
     lib.jsv_tree_attention_kv8.restype = ctypes.c_int
+    lib.jsv_tree_attention_kv8_plan.argtypes = [bp, kp, ctypes.POINTER(jsv_kv8_plan)]
+    lib.jsv_tree_attention_kv8_plan.restype = ctypes.c_int
     lib.jsv_kv8_quantize.argtypes = [bp, kp, vp, vp, vp, vp, vp]
     lib.jsv_kv8_quantize.restype = ctypes.c_int
     lib.jsv_pages_workspace_size.argtypes = [i32, i32]
@@ -305,6 +311,15 @@ def make_kv8(*, format, num_pages, max_pages_per_req, k, v, k_scale, v_scale, pa
 
 def jsv_tree_attention_kv8_workspace_size(batch: jsv_batch, cache8: jsv_kv8) -> int:
     return int(load().jsv_tree_attention_kv8_workspace_size(ctypes.byref(batch), ctypes.byref(cache8)))
+
+
+def jsv_tree_attention_kv8_plan(batch: jsv_batch, cache8: jsv_kv8) -> jsv_kv8_plan:
+    """The form and the splits that ``jsv_tree_attention_kv8`` takes for this
+    geometry; see include/jsv.h."""
+    plan = jsv_kv8_plan()
+    st = load().jsv_tree_attention_kv8_plan(ctypes.byref(batch), ctypes.byref(cache8), ctypes.byref(plan))
+    _check("jsv_tree_attention_kv8_plan", st)
+    return plan
 
 
 def jsv_tree_attention_kv8(batch, cache8, q, k_cache, v_cache, scale, out, workspace, workspace_bytes=None,
