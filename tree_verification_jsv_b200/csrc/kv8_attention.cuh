@@ -61,7 +61,7 @@ __device__ __forceinline__ int unit_tile(int u, int pre_tiles) {
 // Splits of a request of `units`: about C units each, at most S.
 __device__ __forceinline__ int unit_splits(int units, int C, int S) { return max(1, min(S, (units + C - 1) / C)); }
 
-// A K scale as read: an infinite one makes NaN of the codes that are zero, and
+// A K scale as it is used: an infinite one makes NaN of the codes that are zero, and
 // so of the scores, whatever the sign of their finished sums.
 __device__ __forceinline__ float finite_or_nan(float s) { return fabsf(s) < INFINITY ? s : __uint_as_float(0x7fc00000u); }
 

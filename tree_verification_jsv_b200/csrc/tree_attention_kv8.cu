@@ -155,7 +155,7 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (page >= 0 && page < p.c.num_pages) {
                 const size_t block = (size_t)page * a.Hkv + g;
                 row = (int)block * 16;
-                ks = finite_or_nan(__ldg(p.c.k_scale + block));
+                ks = __ldg(p.c.k_scale + block);
                 vs = __ldg(p.c.v_scale + block);
             } else {
                 flag_error(a.dev_status, JSV_ERR_DEVICE_INPUT);
@@ -342,13 +342,14 @@ kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         return vs * vmul;
     };
 
+    ks_c = finite_or_nan(ks_c);                  // here and not where it is loaded, which would wait for it
     bool ok = true;
     volatile int never = 0;
     for (int i = 0; i < count; ++i) {
         const int grp = i >> 5;
         if ((i & 31) == 0 && i > 0) {
             row_c = row_n;
-            ks_c = ks_n;
+            ks_c = finite_or_nan(ks_n);
             vs_c = vs_n;
             load_group(grp + 1, page_n, row_n, ks_n, vs_n);
             page_n = look_up(grp + 2);

@@ -443,7 +443,7 @@ kv8_tiles_kernel(const Kv8Params p) {
             ks = vs = 0.f;
             if (pages >= 0) {
                 const size_t block = (size_t)pages * a.Hkv + g;
-                if constexpr (!is_v) ks = finite_or_nan(__ldg(p.c.k_scale + block));
+                if constexpr (!is_v) ks = __ldg(p.c.k_scale + block);
                 vs = __ldg(p.c.v_scale + block);
             }
         };
@@ -460,14 +460,14 @@ kv8_tiles_kernel(const Kv8Params p) {
             top = __shfl_sync(0xffffffffu, top, 0);
             if (top > kMinScale) refer(fmaxf(top * 0.015625f, kMinScale));
             float ratio = vs * vinv;
-            const bool tiny = fabsf(ratio) < kTinyRatio;
+            const bool tiny = ratio != 0.f && fabsf(ratio) < kTinyRatio;
             if (tiny) ratio *= 1.f / kTinyRatio;
             ok = wait_for(landed, j & 1) && stage_free(j);
             if (!ok) break;
             if (!is_v && me == 0) {
                 TileInfo &ti = info[j % kSlots];
                 if (lane < kTilePages)                       // a page past the prefix: its columns are masked
-                    ti.ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? ks : 1.f;
+                    ti.ks[lane] = (t_begin + j) * kTilePages + lane < pages8 ? finite_or_nan(ks) : 1.f;
                 if (lane == 0) {
                     ti.vref = vref;
                     ti.vinv = vinv;
