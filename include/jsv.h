@@ -408,7 +408,8 @@ JSV_API jsv_status jsv_tree_attention_kv8_plan(const jsv_batch *batch, const jsv
  * infinity or NaN is written with scale NaN and zero codes, and
  * JSV_ERR_DEVICE_INPUT goes to dev_status.  Other pages of the 8-bit cache
  * are left as they are.  Of the batch, B, Hkv, D, num_pages, the page table
- * and dev_status are used.  A request whose lengths are not
+ * and dev_status are used (the other fields are checked on the host as for any
+ * call).  A request whose lengths are not
  * 0 <= from_len <= to_len or need a page past either table's row, or a page
  * whose entry is out of range, is flagged (JSV_ERR_DEVICE_INPUT) and skipped.
  * Two requests must not write the same 8-bit page in one call; one that asks
@@ -468,11 +469,12 @@ JSV_API jsv_status jsv_pages_alloc(const jsv_page_pool *pool, int32_t *page_tabl
  * pair goes to copy_src[i], copy_dst[i] for jsv_pages_copy (-1, -1 where
  * nothing is to be copied).  With full_only != 0 the partial page is left
  * out (a table of 8-bit pages, which are always full).
- * Row dst must be wholly unmapped, appear once among dst, and be no fork's
- * src; else, and where the partial page of src is unmapped or an entry is
- * out of range or free, fork i is skipped and JSV_ERR_DEVICE_INPUT written
- * (of forks with the same dst the first is made).  A fork that does not get
- * its page is skipped with JSV_ERR_NO_PAGES.
+ * Row dst must be wholly unmapped and appear once among dst, and row src be
+ * no fork's dst; else, and where the partial page of src is unmapped or an
+ * entry is out of range or free, fork i is skipped and JSV_ERR_DEVICE_INPUT
+ * written (of forks with the same dst the first is made; a fork into a row
+ * that another names as its src is made, the other is not).  A fork that does
+ * not get its page is skipped with JSV_ERR_NO_PAGES.
  *   src, dst, len        device [n] int32, 0 <= n <= JSV_PAGES_MAX_ROWS
  *   copy_src, copy_dst   device [n] int32
  */

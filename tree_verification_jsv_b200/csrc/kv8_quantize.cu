@@ -158,8 +158,9 @@ kv8_quantize_kernel(const QuantParams p) {
         // overflows (exact, but for what has code 0)
         const float size = amax > 1.0e30f ? 2.3283064365386963e-10f : amax < 1.0e-30f ? 1.8446744073709552e19f : 1.f;
         const float mul = size * kQmax, div = m ? amax * size : 1.f, inv = 1.f / div;
-        // y / div from the reciprocal: the remainder of the first quotient is
-        // exact in one fma, and corrects it to 2^-24 and, where the quotient is
+        // y / div from the reciprocal by Markstein's correction (P. Markstein,
+        // IBM Journal of Research and Development 34, 1990): the remainder of the
+        // first quotient is exact in one fma, and corrects it to 2^-24 and, where the quotient is
         // a number of few bits (a tie between two codes), to that number
         auto code = [&](float x) {
             const float y = x * mul, q = y * inv;
