@@ -15,7 +15,7 @@
 // whole rows of the cache.  Bound by HBM traffic at prefill sizes (2 bytes in,
 // 1 out a value: four prompts of 9,000 to 16,000 tokens take 59 us, 4.6 TB/s, 70% of
 // the measured copy rate) and by launch latency after a verify step, where a
-// request completes a page or none (8 us under ncu).  64 registers, for 32
+// request completes a page or none (6.6 us under ncu).  64 registers, for 32
 // resident warps; 32-bit item indexes and the quotient from one reciprocal a
 // block took prefill from 109 us to that.
 #include "jsv_internal.cuh"

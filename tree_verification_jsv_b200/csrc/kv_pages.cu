@@ -14,9 +14,9 @@
 // cluster barrier (which also orders global memory inside the cluster) takes
 // the place of a second launch between the scan and its use.  Bound by
 // latency: two or three rounds of dependent loads and as many barriers (alloc
-// 8-9 us, fork 12 us, compact 11-13 us under ncu on pools of 300 to 20,000
-// pages; rows' entries are read eight to a lane at a time, which took a fork of
-// 64 rows from 30 us to 20).  Trimming (4 us) and copying need no order between
+// 8-10 us, fork 10 us for 4 rows and 21 for 64, compact 11-14 us under ncu on
+// pools of 300 to 20,000 pages; rows' entries are read eight to a lane at a time,
+// which took the fork of 64 rows from 30 us to 21).  Trimming (4-5 us) and copying need no order between
 // CTAs and use plain grids.
 #include "jsv_internal.cuh"
 #include "kv_internal.cuh"

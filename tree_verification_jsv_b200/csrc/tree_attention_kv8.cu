@@ -78,8 +78,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // about 12 us beside the pages (a chain of dependent loads, the merges, the
 // second launch).  One token of 16 requests over 512 to 8192 tokens (int8, 154
 // MB) takes 36 us, 4.2 TB/s, 65% of the measured copy rate; over 4096 tokens
-// each (e4m3) 34 us.  Rows to 16 by the MMA's M, as first built: 70 us for the
-// former.  Three stages, eight warps a CTA, five CTAs an SM: no better.
+// each (e4m3) 32 us; both under host bounds that fit the batch (see plan_of).
+// Rows to 16 by the MMA's M, as first built: 70 us for the former.  Three stages,
+// eight warps a CTA, five CTAs an SM: no better.
 constexpr int kRowWarps = 4;
 constexpr int kRowStages = 2;
 
@@ -682,17 +683,17 @@ namespace {
 // The page-streaming form costs by (page, KV head, 8 rows), the tcgen05 form by
 // (tile, KV head, 256 rows) and a fixed 15 us or so.  Up to 32 rows of a KV
 // head the first is taken whatever the length (32 heads over 8 KV heads, us,
-// streaming against tcgen05: 8 nodes over 32768 tokens 41 / 51, 16 requests of
-// 8 nodes over 4096 71 / 85), above that while there are few such units (16
-// nodes over 2048, 8,300 units: 17 / 21; 12 over 8192, 25,000: 25 / 29; 4 x 32
-// over 1024, 34,000: 27 / 24; 32 over 8192, 66,000: 39 / 31).
+// streaming against tcgen05: 8 nodes over 32768 tokens 38 / 47, 16 requests of
+// 8 nodes over 4096 67 / 81), above that while there are few such units (16
+// nodes over 2048, 8,300 units: 17 / 21; 12 over 8192, 25,000: 25 / 28; 4 x 32
+// over 1024, 34,000: 29 / 23; 32 over 8192, 66,000: 38 / 30).
 constexpr int kStreamRows = 32;
 constexpr double kStreamUnits = 28000.0;
 // A warp takes 16 rows of a page together once there are enough units to go
-// round (16 requests of 4 nodes over 4096 tokens, 66,000 units: 42 us against 50
+// round (16 requests of 4 nodes over 4096 tokens, 66,000 units: 40 us against 48
 // with 8 rows), 8 otherwise: twice the warps, and half the code to fetch, which
-// is what a short call waits for (16 nodes over 128 tokens 6.9 us against 7.3;
-// 12 over 2048, 6,200 units: 15 against 19).
+// is what a short call waits for (16 nodes over 128 tokens 8.2 us against 10.5;
+// 12 over 2048, 6,200 units: 14 against 18).
 constexpr double kWideUnits = 16000.0;
 
 struct Kv8Plan {
@@ -719,7 +720,13 @@ void choose_splits(Kv8Plan &pl, long long ctas, double load, int total, int most
 }
 
 // From the host-side fields: the largest request's bounds, and the pages that
-// there are for all of them.
+// there are for all of them.  So the splits fit a batch only as well as these
+// do.  A pool with pages to spare hides that a batch is ragged (one token of 16
+// requests over 512 to 8192 tokens: 36 us with a pool that it fills, 51 with one
+// four times as large; a ragged batch of trees 209 and 234; requests of one
+// length as before), and a max_prefix far above the prefixes makes the splits
+// long (four times: 64 us and 262 us for those two, 83 against 38 for 8 nodes
+// over 32768 tokens).
 Kv8Plan plan_of(const BatchArgs &a, const jsv_kv8 &c) {
     Kv8Plan pl;
     const int rows = a.max_nodes * (a.Hq / a.Hkv);

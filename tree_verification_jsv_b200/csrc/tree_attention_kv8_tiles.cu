@@ -8,7 +8,8 @@
 // CTA has 128 rows or fewer, both groups take the same rows and every other
 // tile each, and their results are merged at the end: one group alone would
 // leave the tensor core idle during its softmax (16 requests of 16 nodes over
-// 4096 tokens: 88 us with one group, 83 with two, which the conversion bounds).
+// 4096 tokens: 88 us with one group, 83 with two as first built and 82 now, which
+// the conversion bounds).
 // Also different is where the operands come from: the codes are copied a page
 // at a time to shared memory and written from there to the operand tiles as
 // fp16 by seven converting warps, one 128-key tile ahead, so that the tensor
@@ -45,9 +46,11 @@
 // need no conversion, takes 3,600.  All warps' code of a tile competes for the
 // instruction caches, so what runs rarely is kept out of the loops: a division's
 // rare cases cost 6%, the last tile's mask 3-4%, unrolled conversion 13%.
-// 256 nodes over 16384 tokens (int8) take 109 us (631 TFLOP/s, 38% of the
-// measured bf16 rate), four 512-node trees over 32768 1,264-1,316 us (835-870,
-// by the box's clock), a ragged batch of 16 210 us.
+// 256 nodes over 16384 tokens (int8) take 108 us (636 TFLOP/s, 39% of the
+// measured bf16 rate), four 512-node trees over 32768 1,242-1,294 us (850-885,
+// by the box's clock), a ragged batch of 16 209 us.  The bf16 kernel, with twice
+// the bytes to read and nothing to convert, takes 83, 1,001 and 138 on the same
+// box: this form is for the bytes that the cache holds, not for time.
 #include "kv8_attention.cuh"
 
 #include <type_traits>
