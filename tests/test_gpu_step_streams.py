@@ -53,3 +53,20 @@ def test_run_host_keeps_its_copies_on_the_stream_it_is_given(kind, raw):
     assert all(torch.equal(out[k], v) for k, v in lens.items())
     torch.cuda.synchronize()
     assert np.array_equal(bits(st.out), want) and int(st.status.item()) == 0
+
+
+@pytest.mark.parametrize("kind", ["VerifyStep", "VerifyStepKv8"])
+def test_run_host_on_the_default_stream_by_its_handle(kind):
+    from tree_verification_jsv_b200 import step
+    wl, tokens, _ = golden_workload("tiny")
+    st = getattr(step, kind)(wl, tokens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        out = st.run_host(0)
+        torch.cuda.default_stream().synchronize()
+        assert not side.query()                     # nothing of the step waited for it
+    got = {k: v.clone() for k, v in out.items()}
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, getattr(st, k).cpu()) for k, v in got.items()) and int(st.status.item()) == 0

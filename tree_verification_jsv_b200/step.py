@@ -33,9 +33,11 @@ def _i32(x, device):
 
 
 def _on(stream):
-    """Torch's current stream for a while: a torch stream, a raw handle, or None
-    for the one that is current already."""
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    """Torch's current stream for a while: a torch stream, a raw handle (0: the
+    default stream), or None for the one that is current already."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _bf16(bits, device):
